@@ -38,6 +38,11 @@
  *     the calls): sq_row_absmax, sq_dequant_i32;
  *   - LLM.int8()'s decomposition as a comparator on the same inputs
  *     ([LLMint8] "Fix 1"): sq_llmint8_outliers, sq_llmint8_combine;
+ *   - layers whose MLP is a set of experts: sq_moe_route (the experts of every
+ *     token, and the rows sorted by expert), sq_w8a8_gemm_grouped /
+ *     sq_fp8_gemm_grouped (every expert's rows by its own weights), and
+ *     sq_block_norm_quant_per_token (the weighted sum of a token's rows, the
+ *     norms behind and before a block, gate, scaled residual, INT8 / FP8 codes);
  *   - planning and allocation-free variants: sq_w8a8_gemm_plan,
  *     sq_w8a8_gemm_workspace_size, sq_w8a8_gemm_dequant_noalloc; the two
  *     halves of step 2 (sq_weight_column_max, sq_smooth_scales_from_maxima).
@@ -634,6 +639,160 @@ sq_status sq_w8a8_gemm_dequant_noalloc(const int8_t* Xq, const int8_t* Wq,
                                        const float* x_scale, const float* w_scale, int64_t M,
                                        int64_t N, int64_t K, sq_epilogue epi, void* out,
                                        int64_t ldo, int path_hint, int split_k, void* stream);
+
+/*
+ * Layers whose MLP is a set of experts, in W8A8.  (The source pages treat dense
+ * blocks; these three operators carry their scheme -- per-token activation
+ * scales, per-output-channel weight scales, 8-bit products, both scales in the
+ * epilogue -- over to a block whose tokens choose among E experts.)  One MoE
+ * layer is: codes of the normed tokens (sq_norm_smooth_quant_per_token, or the
+ * block call below), sq_moe_route on the router's logits, the grouped gate/up
+ * GEMM gathering its tokens through row_token, sq_silu_mul_quant_per_token on
+ * its rows, the grouped down GEMM, and sq_block_norm_quant_per_token, which
+ * sums each token's rows and ends in the next layer's codes.
+ *
+ * sq_moe_route -- top-k experts of every token, and the (token, expert) rows
+ * sorted by expert.
+ *   logits   device [T, E] fp32 or bf16 (dtype), row stride ld >= E, element
+ *            aligned; 1 <= E <= SQ_MOE_MAX_EXPERTS
+ *   top_k    1 .. min(E, SQ_MOE_MAX_TOP_K)
+ *   score    SQ_MOE_SOFTMAX: p_e = exp(l_e - max l) / sum over all experts;
+ *            SQ_MOE_SIGMOID: p_e = 1 / (1 + exp(-l_e))
+ *   bias     device [E] fp32 or NULL; SQ_MOE_SIGMOID only: the experts are
+ *            chosen by p_e + bias[e] (compared in fp64), weighted by p_e alone
+ *   renormalize  non-zero: the chosen experts' weights are divided by their sum
+ *            (a sum of 0 gives weights 0)
+ *   scale    multiplies every weight (finite)
+ *   weights  device [T, top_k] fp32 OUT;  experts device [T, top_k] int32 OUT,
+ *            in descending order of choice, equal ones by the lower index
+ *   offsets  device [E + 1] int32 OUT: expert e's rows are [offsets[e],
+ *            offsets[e + 1]), in ascending token order
+ *   row_token  device [T * top_k] int32 OUT: the token of each row
+ *   token_row  device [T, top_k] int32 OUT: the row of each token's j-th expert
+ *   workspace  device scratch of at least sq_moe_route_workspace_size(T, E,
+ *            top_k) bytes, 4-byte aligned (NULL when that is 0); nothing in it
+ *            outlives the call or has to start at any value, and two calls
+ *            that overlap on the GPU need two
+ * An expert whose logit is -inf or NaN (or whose biased score is) is never
+ * chosen -- a padded token with all logits at -inf goes nowhere; +inf counts
+ * as the largest finite value.  Where a token has fewer than top_k experts
+ * left, its last entries are experts = -1, weights = 0, token_row = -1, and
+ * row_token is -1 behind offsets[E].
+ * Errors: SQ_ERR_INVALID_ARG, SQ_ERR_UNSUPPORTED (E, top_k, T * top_k >= 2^31),
+ *         SQ_ERR_ALIGNMENT, SQ_ERR_WORKSPACE, SQ_ERR_CUDA.
+ */
+#define SQ_MOE_MAX_EXPERTS 512
+#define SQ_MOE_MAX_TOP_K 16
+
+typedef enum { SQ_MOE_SOFTMAX = 0, SQ_MOE_SIGMOID = 1 } sq_moe_score;
+
+size_t sq_moe_route_workspace_size(int64_t T, int64_t E, int top_k);
+
+sq_status sq_moe_route(const void* logits, sq_dtype dtype, int64_t T, int64_t E, int64_t ld,
+                       int top_k, sq_moe_score score, const float* bias, int renormalize,
+                       float scale, float* weights, int32_t* experts, int32_t* offsets,
+                       int32_t* row_token, int32_t* token_row, void* workspace,
+                       size_t ws_bytes, void* stream);
+
+/*
+ * sq_w8a8_gemm_grouped -- sq_w8a8_gemm_dequant for rows grouped by expert, each
+ * group with its own weights: for offsets[e] <= r < offsets[e + 1]
+ *   acc[r, n] = sum_k Xq[src(r), k] * Wq[e, n, k]  (exact INT32),
+ *   out[r, n] = bf16(fl32(fl32(fl32(acc) * x_scale[src(r)]) * w_scale[e, n])),
+ * src(r) = row_token[r], or r where row_token is NULL.
+ *   Xq       device [X, K] int8 (stride K); without row_token X >= R
+ *   Wq       device [E, N, K] int8 (dense);  w_scale device [E, N] fp32
+ *   x_scale  device [X] fp32 (both scales ignored for SQ_EPI_I32_RAW)
+ *   offsets  device [E + 1] int32, ascending (sq_moe_route's); values are
+ *            clamped to [0, R].  The group sizes stay on the device: nothing
+ *            is read back, and an empty expert's weights are not read
+ *   row_token  device [R] int32 or NULL; a row whose token is outside [0, X)
+ *            is a row of zeros
+ *   epi      SQ_EPI_BF16, SQ_EPI_BF16_RELU or SQ_EPI_I32_RAW
+ *   out      device [R, N], row stride ldo; rows outside [offsets[0],
+ *            offsets[E]) are left as they were
+ *   path_hint  0 = automatic, 1 = prefill tiles (CTA pairs), 2 = decode tiles
+ *            (weight blocks of 128 rows, K split over a small cluster)
+ * E <= SQ_MOE_MAX_EXPERTS.
+ * Errors: those of sq_w8a8_gemm_dequant.
+ */
+sq_status sq_w8a8_gemm_grouped(const int8_t* Xq, int64_t X, const int8_t* Wq,
+                               const float* x_scale, const float* w_scale,
+                               const int32_t* offsets, const int32_t* row_token, int64_t R,
+                               int64_t E, int64_t N, int64_t K, sq_epilogue epi, void* out,
+                               int64_t ldo, int path_hint, void* stream);
+
+/*
+ * sq_fp8_gemm_grouped -- the same on e4m3 codes with an fp32 accumulator (as
+ * sq_fp8_gemm_dequant; the raw epilogue is SQ_EPI_F32_RAW).  K ranges split
+ * over a cluster are added in a fixed order.
+ */
+sq_status sq_fp8_gemm_grouped(const uint8_t* Xq8, int64_t X, const uint8_t* Wq8,
+                              const float* x_scale, const float* w_scale,
+                              const int32_t* offsets, const int32_t* row_token, int64_t R,
+                              int64_t E, int64_t N, int64_t K, sq_epilogue epi, void* out,
+                              int64_t ldo, int path_hint, void* stream);
+
+/*
+ * sq_block_norm_quant_per_token -- the end of one block and the start of the
+ * next in one pass over the rows: for every token m
+ *   c = x[m], or, behind a layer of experts, sum_j weights[m, j] *
+ *       x[token_row[m, j]] (entries outside [0, R) are skipped, never read)
+ *   u = post_norm(c)                        (the norm behind the block)
+ *   h = residual_scale * residual[m] + u * gate * token_gate[m]
+ *   y = pre_norm(h)                         (the norm before the next block,
+ *                                            its gamma folded with 1/s)
+ *   x_scale[m] = fl32(max |y| / 127), Xq[m] = clamp(rne(fl32(y / x_scale[m])))
+ *   h_out[m] = h rounded to dtype.
+ * [SQ-depth] "Where the scales go in a decoder block": 1/s folds into the norm
+ * in front of a Linear; "Granularity": per-token scales.
+ * Everything between the inputs and the codes is fp32 (sums and statistics
+ * too; h is not rounded before pre_norm reads it; LayerNorm's variance is
+ * taken around the mean).  The order of every sum depends on K and top_k
+ * alone, or on M as well through the launch shape; it never depends on timing.
+ * A row with a NaN or an infinity gets a non-finite x_scale.
+ */
+typedef struct sq_block_norm_args {
+  const void* x;            /* device [R, K] (R = M without token_row), stride ldx */
+  int64_t ldx;
+  int64_t R;                /* rows of x (with token_row) */
+  const int32_t* token_row; /* device [M, top_k], or NULL: no weighted sum */
+  const float* weights;     /* device [M, top_k] fp32 (with token_row) */
+  int top_k;                /* 1 .. SQ_MOE_MAX_TOP_K with token_row, else 0 */
+  sq_dtype dtype;           /* of x, residual and h_out: fp32 or bf16 */
+  int64_t M, K;             /* K % 16 == 0, K <= SQ_BLOCK_NORM_MAX_K */
+  sq_norm post_norm;        /* SQ_NORM_NONE / RMS / LAYER */
+  const float* post_gamma;  /* device [K] fp32 or NULL (= 1; with NONE a multiplier) */
+  const float* post_beta;   /* device [K] fp32 or NULL (= 0; LayerNorm only) */
+  float post_eps;
+  const float* gate;        /* device [K] fp32 or NULL (= 1) */
+  const float* token_gate;  /* device [M] fp32 or NULL (= 1) */
+  const void* residual;     /* device [M, K], stride ld_res, or NULL (= 0) */
+  int64_t ld_res;
+  float residual_scale;
+  sq_norm pre_norm;
+  const float* pre_gamma;
+  const float* pre_beta;
+  float pre_eps;
+  void* h_out;              /* device [M, K], stride ld_h, or NULL; may be residual
+                               itself (same stride), or x itself without token_row */
+  int64_t ld_h;
+  void* Xq;                 /* device [M, K] codes (dense), or NULL: h_out alone */
+  float* x_scale;           /* device [M] fp32 (with Xq) */
+} sq_block_norm_args;
+
+#define SQ_BLOCK_NORM_MAX_K 32768
+
+/*
+ * Input rows and vectors 16-byte aligned as everywhere; Xq int8 (e4m3 bytes for
+ * the _fp8 call: step = fl32(max |y| / 448), codes e4m3(fl32(y * fl32(1 / step))),
+ * a zero or subnormal step gives step 0 and zero codes).
+ * Errors: SQ_ERR_INVALID_ARG (among them an h_out that overlaps x or residual
+ *         otherwise than allowed above, or Xq overlapping an input),
+ *         SQ_ERR_ALIGNMENT, SQ_ERR_UNSUPPORTED, SQ_ERR_CUDA.
+ */
+sq_status sq_block_norm_quant_per_token(const sq_block_norm_args* args, void* stream);
+sq_status sq_block_norm_quant_per_token_fp8(const sq_block_norm_args* args, void* stream);
 
 /* Human-readable name of a status code (static storage). */
 const char* sq_status_string(sq_status status);

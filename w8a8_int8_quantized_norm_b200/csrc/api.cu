@@ -45,6 +45,7 @@ int sms_cached() {
 }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 inline bool valid_dtype(int d) { return d == SQ_F32 || d == SQ_BF16; }
 inline bool valid_norm(int n) { return n == SQ_NORM_NONE || n == SQ_NORM_RMS || n == SQ_NORM_LAYER; }
 inline int64_t dsize(int d) { return d == SQ_BF16 ? 2 : 4; }
@@ -599,6 +600,146 @@ sq_status sq_linear_w8a8(const void* x, sq_dtype dtype, int64_t M, int64_t K, in
   if (e != cudaSuccess) return SQ_ERR_CUDA;
   return from_cuda(launch_gemm(plan, Xq_scratch, Wq, xscale_scratch, w_scale, M, N, K, epi, out,
                                ldo, workspace, sms, g_wait_polls.load(), err, cs));
+}
+
+// ---------------------------------------------------------------------------
+// layers of experts
+// ---------------------------------------------------------------------------
+
+size_t sq_moe_route_workspace_size(int64_t T, int64_t E, int top_k) {
+  if (T <= 0 || E <= 0 || E > SQ_MOE_MAX_EXPERTS || top_k <= 0) return 0;
+  return moe_route_workspace(T, E);
+}
+
+sq_status sq_moe_route(const void* logits, sq_dtype dtype, int64_t T, int64_t E, int64_t ld,
+                       int top_k, sq_moe_score score, const float* bias, int renormalize,
+                       float scale, float* weights, int32_t* experts, int32_t* offsets,
+                       int32_t* row_token, int32_t* token_row, void* workspace,
+                       size_t ws_bytes, void* stream) {
+  if (!valid_dtype(dtype) || T < 0 || E <= 0 || ld < E || top_k <= 0 || top_k > E)
+    return SQ_ERR_INVALID_ARG;
+  if (score != SQ_MOE_SOFTMAX && score != SQ_MOE_SIGMOID) return SQ_ERR_INVALID_ARG;
+  if ((bias && score != SQ_MOE_SIGMOID) || !isfinite(scale) || !offsets) return SQ_ERR_INVALID_ARG;
+  if (T > 0 && (!logits || !weights || !experts || !row_token || !token_row))
+    return SQ_ERR_INVALID_ARG;
+  if (E > SQ_MOE_MAX_EXPERTS || top_k > SQ_MOE_MAX_TOP_K || T > 0x7fffffff / top_k)
+    return SQ_ERR_UNSUPPORTED;
+  if (reinterpret_cast<uintptr_t>(logits) % dsize(dtype) || !aligned4(bias) || !aligned4(weights) ||
+      !aligned4(experts) || !aligned4(offsets) || !aligned4(row_token) || !aligned4(token_row) ||
+      !aligned4(workspace))
+    return SQ_ERR_ALIGNMENT;
+  const size_t need = moe_route_workspace(T, E);
+  if (need > 0 && (!workspace || ws_bytes < need)) return SQ_ERR_WORKSPACE;
+  return from_cuda(launch_moe_route(logits, dtype == SQ_BF16, T, static_cast<int>(E), ld, top_k,
+                                    score == SQ_MOE_SIGMOID, bias, renormalize != 0, scale, weights,
+                                    experts, offsets, row_token, token_row, workspace,
+                                    as_stream(stream)));
+}
+
+namespace {
+
+sq_status gemm_grouped(const void* Xq, int64_t X, const void* Wq, const float* x_scale,
+                       const float* w_scale, const int32_t* offsets, const int32_t* row_token,
+                       int64_t R, int64_t E, int64_t N, int64_t K, int epi, void* out, int64_t ldo,
+                       int path_hint, bool fp8, void* stream) {
+  const int raw = fp8 ? SQ_EPI_F32_RAW : SQ_EPI_I32_RAW;
+  if (X < 0 || R < 0 || E <= 0 || N < 0 || K <= 0 || ldo < N) return SQ_ERR_INVALID_ARG;
+  if (epi != SQ_EPI_BF16 && epi != SQ_EPI_BF16_RELU && epi != raw) return SQ_ERR_INVALID_ARG;
+  if (path_hint < 0 || path_hint > 2) return SQ_ERR_INVALID_ARG;
+  if (!row_token && X < R) return SQ_ERR_INVALID_ARG;
+  if (E > SQ_MOE_MAX_EXPERTS) return SQ_ERR_UNSUPPORTED;
+  if (R == 0 || N == 0) return SQ_OK;
+  if (X == 0 || !Xq || !Wq || !out || !offsets) return SQ_ERR_INVALID_ARG;
+  if (epi != raw && (!x_scale || !w_scale)) return SQ_ERR_INVALID_ARG;
+  if (K > SQ_MAX_K) return SQ_ERR_OVERFLOW_RISK;
+  // tensor-map coordinates and row numbers are 32-bit
+  if (X > 0x7fffffff || R > 0x7fffffff || N > 0x7fffffff / E) return SQ_ERR_UNSUPPORTED;
+  const uintptr_t esz = epi == raw ? 4 : 2;
+  if (K % 16 != 0 || !aligned16(Xq) || !aligned16(Wq) ||
+      reinterpret_cast<uintptr_t>(out) % esz != 0 || !aligned4(x_scale) || !aligned4(w_scale) ||
+      !aligned4(offsets) || !aligned4(row_token))
+    return SQ_ERR_ALIGNMENT;
+  int* err = device_error_word();
+  if (!err) return SQ_ERR_CUDA;
+  return from_cuda(launch_gemm_grouped(Xq, X, Wq, x_scale, w_scale, offsets, row_token, R, E, N, K,
+                                       epi, out, ldo, path_hint, g_wait_polls.load(), err, fp8,
+                                       as_stream(stream)));
+}
+
+// Bytes [p, p + n) against [q, q + m).
+bool overlap(const void* p, int64_t n, const void* q, int64_t m) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return p && q && n > 0 && m > 0 && a < b + static_cast<uintptr_t>(m) &&
+         b < a + static_cast<uintptr_t>(n);
+}
+
+sq_status block_norm(const sq_block_norm_args* args, bool fp8, void* stream) {
+  if (!args) return SQ_ERR_INVALID_ARG;
+  const sq_block_norm_args& a = *args;
+  if (!valid_dtype(a.dtype) || a.M < 0 || a.K <= 0) return SQ_ERR_INVALID_ARG;
+  if (!valid_norm(a.post_norm) || !valid_norm(a.pre_norm) || !(a.post_eps >= 0.0f) ||
+      !(a.pre_eps >= 0.0f))
+    return SQ_ERR_INVALID_ARG;
+  if (!a.h_out && !a.Xq) return SQ_ERR_INVALID_ARG;
+  const bool sum = a.token_row != nullptr;
+  if (sum != (a.weights != nullptr) || sum != (a.top_k > 0) || a.top_k < 0)
+    return SQ_ERR_INVALID_ARG;
+  if (sum && a.R < 0) return SQ_ERR_INVALID_ARG;
+  if (a.top_k > SQ_MOE_MAX_TOP_K || a.K > SQ_BLOCK_NORM_MAX_K) return SQ_ERR_UNSUPPORTED;
+  const int64_t rows = sum ? a.R : a.M;
+  // rows, strides, alignment of the row inputs and of h_out
+  sq_status st = check_rows(a.x, a.dtype, rows, a.K, a.ldx);
+  if (st != SQ_OK) return st;
+  if (a.M > 0x7fffffff) return SQ_ERR_UNSUPPORTED;
+  if (a.residual && (st = check_rows(a.residual, a.dtype, a.M, a.K, a.ld_res)) != SQ_OK) return st;
+  if (a.h_out && (st = check_rows(a.h_out, a.dtype, a.M, a.K, a.ld_h)) != SQ_OK) return st;
+  for (const float* v : {a.post_gamma, a.post_beta, a.gate, a.pre_gamma, a.pre_beta})
+    if ((st = check_vec(v, false)) != SQ_OK) return st;
+  if (!aligned4(a.token_row) || !aligned4(a.weights) || !aligned4(a.token_gate) ||
+      !aligned4(a.x_scale) || !aligned16(a.Xq))
+    return SQ_ERR_ALIGNMENT;
+  if (a.M == 0) return SQ_OK;
+  if (a.Xq && !a.x_scale) return SQ_ERR_INVALID_ARG;
+  // a row may be replaced by its own output, nothing else may share memory
+  const int64_t es = dsize(a.dtype);
+  const int64_t nx = rows > 0 ? ((rows - 1) * a.ldx + a.K) * es : 0;
+  const int64_t nr = ((a.M - 1) * a.ld_res + a.K) * es, nh = ((a.M - 1) * a.ld_h + a.K) * es;
+  if (overlap(a.h_out, nh, a.x, nx) && (sum || a.h_out != a.x || a.ld_h != a.ldx))
+    return SQ_ERR_INVALID_ARG;
+  if (overlap(a.h_out, nh, a.residual, nr) && (a.h_out != a.residual || a.ld_h != a.ld_res))
+    return SQ_ERR_INVALID_ARG;
+  if (overlap(a.Xq, a.M * a.K, a.x, nx) || overlap(a.Xq, a.M * a.K, a.residual, nr) ||
+      overlap(a.Xq, a.M * a.K, a.h_out, nh))
+    return SQ_ERR_INVALID_ARG;
+  return from_cuda(launch_block_norm(a, fp8, as_stream(stream)));
+}
+
+}  // namespace
+
+sq_status sq_w8a8_gemm_grouped(const int8_t* Xq, int64_t X, const int8_t* Wq,
+                               const float* x_scale, const float* w_scale,
+                               const int32_t* offsets, const int32_t* row_token, int64_t R,
+                               int64_t E, int64_t N, int64_t K, sq_epilogue epi, void* out,
+                               int64_t ldo, int path_hint, void* stream) {
+  return gemm_grouped(Xq, X, Wq, x_scale, w_scale, offsets, row_token, R, E, N, K, epi, out, ldo,
+                      path_hint, false, stream);
+}
+
+sq_status sq_fp8_gemm_grouped(const uint8_t* Xq8, int64_t X, const uint8_t* Wq8,
+                              const float* x_scale, const float* w_scale,
+                              const int32_t* offsets, const int32_t* row_token, int64_t R,
+                              int64_t E, int64_t N, int64_t K, sq_epilogue epi, void* out,
+                              int64_t ldo, int path_hint, void* stream) {
+  return gemm_grouped(Xq8, X, Wq8, x_scale, w_scale, offsets, row_token, R, E, N, K, epi, out, ldo,
+                      path_hint, true, stream);
+}
+
+sq_status sq_block_norm_quant_per_token(const sq_block_norm_args* args, void* stream) {
+  return block_norm(args, false, stream);
+}
+
+sq_status sq_block_norm_quant_per_token_fp8(const sq_block_norm_args* args, void* stream) {
+  return block_norm(args, true, stream);
 }
 
 }  // extern "C"

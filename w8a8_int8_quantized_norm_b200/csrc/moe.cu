@@ -1,0 +1,349 @@
+// moe.cu -- the router of a layer of experts: each token's top-k experts with
+// their weights, and the (token, expert) rows sorted by expert.
+//
+// Two passes.  The first ranks: a warp per token holds the token's logits in
+// registers (lane l the experts l, l + 32, ...), takes the largest key k
+// times with warp-wide integer maxima (keys are the logits' bits mapped to
+// order like integers, so a maximum costs one redux), and the lowest index
+// among equal keys with a warp-wide minimum.  A CTA walks a contiguous range
+// of tokens in groups of 64; within a group each expert keeps a 64-bit mask of
+// the tokens that chose it (a token chooses an expert at most once), so a
+// row's rank among the group's rows of that expert is a population count --
+// stable in token order whatever order the mask's atomics arrived in.  The
+// second pass adds, per expert, the counts of all earlier CTAs and experts and
+// scatters.  With one CTA's worth of tokens the first pass scatters itself.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <float.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "sq_device.cuh"
+#include "sq_launch.h"
+
+namespace sq {
+namespace {
+
+constexpr int kRouteThreads = 512;
+constexpr int kRouteWarps = kRouteThreads / 32;
+constexpr int kGroup = 64;      // tokens of one mask
+constexpr int kMaxBlocks = 148; // CTAs of the first pass: the second reads all their counts
+constexpr int kMaxExperts = SQ_MOE_MAX_EXPERTS;
+
+struct RouteParams {
+  const void* logits;
+  int64_t T, ld;
+  int E, top_k, sigmoid, renorm;
+  const float* bias;
+  float scale;
+  float* weights;
+  int32_t* experts;
+  int32_t* offsets;
+  int32_t* row_token;
+  int32_t* token_row;
+  int32_t* hist;      // [blocks][E] rows of each expert per CTA of the first pass
+  int blocks;
+  int64_t per_block;  // tokens per CTA, a multiple of kGroup
+};
+
+// Finite floats and +-inf to unsigned integers of the same order.
+__device__ __forceinline__ uint32_t order_key(float v) {
+  const uint32_t b = __float_as_uint(v);
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ uint64_t order_key(double v) {
+  const uint64_t b = static_cast<uint64_t>(__double_as_longlong(v));
+  return (b >> 63) ? ~b : (b | 0x8000000000000000ull);
+}
+
+__device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(~0u, v); }
+__device__ __forceinline__ uint64_t warp_max(uint64_t v) {
+  const uint32_t hi = __reduce_max_sync(~0u, static_cast<uint32_t>(v >> 32));
+  const uint32_t lo = static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u;
+  return (static_cast<uint64_t>(hi) << 32) | __reduce_max_sync(~0u, lo);
+}
+
+__device__ __forceinline__ float sigmoid_f(float l) { return 1.0f / (1.0f + expf(-l)); }
+
+__device__ __forceinline__ float load_logit(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ float load_logit(const float* p) { return *p; }
+
+// One token's choice by one warp: lane j < top_k returns its j-th expert (-1:
+// none left) and its weight.  V: experts per lane.  Key 0 marks an expert that
+// cannot be chosen (every finite value's key is above it).
+template <typename T, int V, bool kBias>
+__device__ __forceinline__ void choose(const RouteParams& p, int64_t t, int lane, int& my_e,
+                                       float& my_w) {
+  using Key = typename std::conditional<kBias, uint64_t, uint32_t>::type;
+  const T* row = static_cast<const T*>(p.logits) + t * p.ld;
+  float l[V];
+  Key key[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = lane + 32 * i;
+    float v = -INFINITY;
+    if (e < p.E) v = load_logit(row + e);
+    if (!(v >= -FLT_MAX)) v = -INFINITY;  // NaN too
+    l[i] = fminf(v, FLT_MAX) + 0.0f;  // -0 becomes +0: the two are equal keys
+  }
+  float m = -FLT_MAX;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const bool ok = l[i] >= -FLT_MAX;
+    m = fmaxf(m, l[i]);
+    if constexpr (kBias) {
+      key[i] = 0;
+      if (ok) {
+        const double s = 1.0 / (1.0 + exp(-static_cast<double>(l[i]))) +
+                         static_cast<double>(p.bias[lane + 32 * i]) + 0.0;
+        if (s > -INFINITY) key[i] = order_key(s);  // false for NaN
+      }
+    } else {
+      key[i] = ok ? order_key(l[i]) : 0;
+    }
+  }
+  float total = 0.0f;
+  if (!p.sigmoid) {
+    // the row's maximum through the order-preserving keys
+    const uint32_t mk = __reduce_max_sync(~0u, order_key(m));
+    m = __uint_as_float((mk & 0x80000000u) ? (mk ^ 0x80000000u) : ~mk);
+    if (!p.renorm) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (l[i] >= -FLT_MAX) total += expf(l[i] - m);
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) total += __shfl_xor_sync(~0u, total, s);
+    }
+  }
+  my_e = -1;
+  my_w = 0.0f;
+  float my_l = 0.0f;
+  for (int j = 0; j < p.top_k; ++j) {
+    Key best = 0;
+    int at = kMaxExperts;
+    float lv = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i)  // ascending index: the first of equal keys stays
+      if (key[i] > best) {
+        best = key[i];
+        at = lane + 32 * i;
+        lv = l[i];
+      }
+    const Key top = warp_max(best);
+    if (top == 0) break;  // nothing left to choose
+    const int e = static_cast<int>(
+        __reduce_min_sync(~0u, static_cast<uint32_t>(best == top ? at : kMaxExperts)));
+    lv = __shfl_sync(~0u, lv, e & 31);
+    if (lane == j) {
+      my_e = e;
+      my_l = lv;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (e == lane + 32 * i) key[i] = 0;
+  }
+  if (my_e >= 0) my_w = p.sigmoid ? sigmoid_f(my_l) : expf(my_l - m);
+  if (p.renorm) {
+    total = my_w;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) total += __shfl_xor_sync(~0u, total, s);
+  } else if (p.sigmoid) {
+    total = 1.0f;
+  }
+  my_w = total > 0.0f ? my_w / total * p.scale : 0.0f;
+}
+
+// Exclusive prefix sum of counts[0 .. E) into offsets[0 .. E] (shared memory),
+// by the first warp.
+__device__ __forceinline__ void scan_offsets(const int* counts, int* offsets, int E, int lane) {
+  int run = 0;
+  for (int e0 = 0; e0 < E; e0 += 32) {
+    const int v = e0 + lane < E ? counts[e0 + lane] : 0;
+    int inc = v;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+      const int u = __shfl_up_sync(~0u, inc, s);
+      if (lane >= s) inc += u;
+    }
+    if (e0 + lane < E) offsets[e0 + lane] = run + inc - v;
+    run += __shfl_sync(~0u, inc, 31);
+  }
+  if (lane == 0) offsets[E] = run;
+}
+
+template <typename T, int V, bool kBias>
+__global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RouteParams p) {
+  __shared__ unsigned long long mask[32 * V];
+  __shared__ int count[32 * V];
+  __shared__ int off[32 * V + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t t_begin = static_cast<int64_t>(blockIdx.x) * p.per_block;
+  const int64_t t_end = min(p.T, t_begin + p.per_block);
+  for (int e = threadIdx.x; e < p.E; e += kRouteThreads) count[e] = 0;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (int64_t g = t_begin; g < t_end; g += kGroup) {
+    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) mask[e] = 0;
+    __syncthreads();
+    int my_e[kGroup / kRouteWarps];
+#pragma unroll
+    for (int i = 0; i < kGroup / kRouteWarps; ++i) {
+      const int64_t t = g + warp + i * kRouteWarps;
+      my_e[i] = -1;
+      if (t < t_end) {
+        float w;
+        choose<T, V, kBias>(p, t, lane, my_e[i], w);
+        if (lane < p.top_k) {
+          p.weights[t * p.top_k + lane] = w;
+          p.experts[t * p.top_k + lane] = my_e[i];
+          if (my_e[i] >= 0) atomicOr(&mask[my_e[i]], 1ull << (warp + i * kRouteWarps));
+        }
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kGroup / kRouteWarps; ++i) {
+      const int tl = warp + i * kRouteWarps;
+      const int64_t t = g + tl;
+      if (t < t_end && lane < p.top_k) {
+        // the row's rank among this CTA's rows of its expert
+        const int r = my_e[i] < 0
+                          ? -1
+                          : count[my_e[i]] + __popcll(mask[my_e[i]] & ((1ull << tl) - 1));
+        p.token_row[t * p.top_k + lane] = r;
+      }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) count[e] += __popcll(mask[e]);
+  }
+  __syncthreads();
+  if (p.blocks > 1) {
+    for (int e = threadIdx.x; e < p.E; e += kRouteThreads)
+      p.hist[static_cast<int64_t>(blockIdx.x) * p.E + e] = count[e];
+    return;
+  }
+  if (warp == 0) scan_offsets(count, off, p.E, lane);
+  __syncthreads();
+  for (int e = threadIdx.x; e <= p.E; e += kRouteThreads) p.offsets[e] = off[e];
+  const int rows = static_cast<int>(p.T) * p.top_k;
+  for (int i = threadIdx.x; i < rows; i += kRouteThreads) {
+    const int e = p.experts[i];
+    if (e >= 0) {
+      const int r = off[e] + p.token_row[i];
+      p.token_row[i] = r;
+      p.row_token[r] = i / p.top_k;
+    }
+  }
+  for (int r = off[p.E] + threadIdx.x; r < rows; r += kRouteThreads) p.row_token[r] = -1;
+}
+
+__global__ void __launch_bounds__(kRouteThreads) moe_scatter_kernel(const RouteParams p) {
+  __shared__ int before[kMaxExperts];  // rows of the earlier CTAs' tokens
+  __shared__ int total[kMaxExperts];
+  __shared__ int off[kMaxExperts + 1];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int b = static_cast<int>(blockIdx.x);
+  for (int e = threadIdx.x; e < p.E; e += kRouteThreads) {
+    int s = 0, all = 0;
+    for (int i = 0; i < p.blocks; ++i) {
+      const int c = p.hist[static_cast<int64_t>(i) * p.E + e];
+      if (i < b) s += c;
+      all += c;
+    }
+    before[e] = s;
+    total[e] = all;
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) scan_offsets(total, off, p.E, static_cast<int>(threadIdx.x));
+  __syncthreads();
+  if (b == 0)
+    for (int e = threadIdx.x; e <= p.E; e += kRouteThreads) p.offsets[e] = off[e];
+  const int64_t i0 = b * p.per_block * p.top_k;
+  const int64_t i1 = min(p.T, (b + 1) * p.per_block) * p.top_k;
+  for (int64_t i = i0 + threadIdx.x; i < i1; i += kRouteThreads) {
+    const int e = p.experts[i];
+    if (e >= 0) {
+      const int r = off[e] + before[e] + p.token_row[i];
+      p.token_row[i] = r;
+      p.row_token[r] = static_cast<int>(i / p.top_k);
+    }
+    if (i >= off[p.E]) p.row_token[i] = -1;  // behind the last expert's rows
+  }
+}
+
+void route_shape(int64_t T, int& blocks, int64_t& per_block) {
+  const int64_t groups = (T + kGroup - 1) / kGroup;
+  const int64_t per = (groups + kMaxBlocks - 1) / kMaxBlocks;
+  per_block = per * kGroup;
+  blocks = static_cast<int>((groups + per - 1) / per);
+}
+
+cudaError_t launch_dependent(const void* kernel, int grid, const RouteParams& p, cudaStream_t st) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kRouteThreads);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  void* args[1] = {const_cast<RouteParams*>(&p)};
+  return cudaLaunchKernelExC(&cfg, kernel, args);
+}
+
+template <typename T, int V>
+const void* pick_bias(bool bias) {
+  return bias ? reinterpret_cast<const void*>(moe_route_kernel<T, V, true>)
+              : reinterpret_cast<const void*>(moe_route_kernel<T, V, false>);
+}
+template <typename T>
+const void* pick_kernel(int E, bool bias) {
+  return E <= 32 ? pick_bias<T, 1>(bias) : E <= 64 ? pick_bias<T, 2>(bias)
+       : E <= 128 ? pick_bias<T, 4>(bias) : E <= 256 ? pick_bias<T, 8>(bias)
+                                                      : pick_bias<T, 16>(bias);
+}
+
+}  // namespace
+
+size_t moe_route_workspace(int64_t T, int64_t E) {
+  if (T <= 0) return 0;
+  int blocks;
+  int64_t per;
+  route_shape(T, blocks, per);
+  return blocks > 1 ? static_cast<size_t>(blocks) * static_cast<size_t>(E) * 4u : 0u;
+}
+
+cudaError_t launch_moe_route(const void* logits, bool bf16, int64_t T, int E, int64_t ld, int top_k,
+                             bool sigmoid, const float* bias, bool renorm, float scale,
+                             float* weights, int32_t* experts, int32_t* offsets,
+                             int32_t* row_token, int32_t* token_row, void* workspace,
+                             cudaStream_t st) {
+  if (T == 0) return cudaMemsetAsync(offsets, 0, static_cast<size_t>(E + 1) * 4u, st);
+  RouteParams p{};
+  p.logits = logits;
+  p.T = T;
+  p.ld = ld;
+  p.E = E;
+  p.top_k = top_k;
+  p.sigmoid = sigmoid;
+  p.renorm = renorm;
+  p.bias = bias;
+  p.scale = scale;
+  p.weights = weights;
+  p.experts = experts;
+  p.offsets = offsets;
+  p.row_token = row_token;
+  p.token_row = token_row;
+  p.hist = static_cast<int32_t*>(workspace);
+  route_shape(T, p.blocks, p.per_block);
+  const void* k = bf16 ? pick_kernel<__nv_bfloat16>(E, bias != nullptr)
+                       : pick_kernel<float>(E, bias != nullptr);
+  cudaError_t e = launch_dependent(k, p.blocks, p, st);
+  if (e == cudaSuccess && p.blocks > 1)
+    e = launch_dependent(reinterpret_cast<const void*>(moe_scatter_kernel), p.blocks, p, st);
+  return e;
+}
+
+}  // namespace sq

@@ -10,6 +10,8 @@
 #include <mutex>
 #include <tuple>
 
+#include "../../include/sq.h"
+
 namespace sq {
 
 // Host-side launch queries (function attributes, occupancy, SM counts) are
@@ -129,6 +131,24 @@ cudaError_t launch_llmint8_combine(const int32_t* acc, int64_t M, int64_t N, int
                                    bool x_bf16, int64_t ldx, const void* W, bool w_bf16,
                                    int64_t ldw, const int32_t* idx, const int32_t* count, int relu,
                                    void* out, int64_t ldo, cudaStream_t st);
+
+// moe.cu (the router of a layer of experts)
+size_t moe_route_workspace(int64_t T, int64_t E);
+cudaError_t launch_moe_route(const void* logits, bool bf16, int64_t T, int E, int64_t ld, int top_k,
+                             bool sigmoid, const float* bias, bool renorm, float scale,
+                             float* weights, int32_t* experts, int32_t* offsets,
+                             int32_t* row_token, int32_t* token_row, void* workspace,
+                             cudaStream_t st);
+
+// grouped.cu (the GEMM of rows grouped by expert)
+cudaError_t launch_gemm_grouped(const void* Xq, int64_t X, const void* Wq, const float* x_scale,
+                                const float* w_scale, const int32_t* offsets,
+                                const int32_t* row_token, int64_t R, int64_t E, int64_t N,
+                                int64_t K, int epi, void* out, int64_t ldo, int path_hint,
+                                int64_t wait_polls, int* error_word, bool fp8, cudaStream_t st);
+
+// blocknorm.cu (the end of one block and the start of the next)
+cudaError_t launch_block_norm(const sq_block_norm_args& a, bool fp8, cudaStream_t st);
 
 // gemm.cu
 struct GemmPlan {

@@ -9,9 +9,10 @@ raised.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
-from typing import Optional, Sequence, Tuple
+from typing import NamedTuple, Optional, Sequence, Tuple
 
 import torch
 
@@ -40,9 +41,14 @@ EXPORTS = (
     "sq_smooth_quantize_weights_fp8", "sq_fp8_gemm_dequant", "sq_weight_column_max",
     "sq_smooth_scales_from_maxima", "sq_silu_mul_quant_per_token_fp8", "sq_row_absmax",
     "sq_dequant_i32", "sq_llmint8_outliers", "sq_llmint8_combine",
+    "sq_moe_route_workspace_size", "sq_moe_route", "sq_w8a8_gemm_grouped", "sq_fp8_gemm_grouped",
+    "sq_block_norm_quant_per_token", "sq_block_norm_quant_per_token_fp8",
 )
 LLMINT8_MAX_K = 1 << 20
 NOALLOC_SCRATCH_BYTES = 8 << 20
+MOE_MAX_EXPERTS, MOE_MAX_TOP_K = 512, 16
+MOE_SCORES = {"softmax": 0, "sigmoid": 1}
+BLOCK_NORM_MAX_K = 32768
 
 
 class GemmPlanInfo(ctypes.Structure):
@@ -57,6 +63,22 @@ class GemmPlanInfo(ctypes.Structure):
         d = {f: getattr(self, f) for f, _ in self._fields_}
         d["kernel_name"] = self.KERNELS[self.kernel]
         return d
+
+
+class BlockNormArgs(ctypes.Structure):
+    """sq_block_norm_args: the arguments of sq_block_norm_quant_per_token."""
+    _fields_ = [("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("R", ctypes.c_int64),
+                ("token_row", ctypes.c_void_p), ("weights", ctypes.c_void_p),
+                ("top_k", ctypes.c_int), ("dtype", ctypes.c_int), ("M", ctypes.c_int64),
+                ("K", ctypes.c_int64), ("post_norm", ctypes.c_int),
+                ("post_gamma", ctypes.c_void_p), ("post_beta", ctypes.c_void_p),
+                ("post_eps", ctypes.c_float), ("gate", ctypes.c_void_p),
+                ("token_gate", ctypes.c_void_p), ("residual", ctypes.c_void_p),
+                ("ld_res", ctypes.c_int64), ("residual_scale", ctypes.c_float),
+                ("pre_norm", ctypes.c_int), ("pre_gamma", ctypes.c_void_p),
+                ("pre_beta", ctypes.c_void_p), ("pre_eps", ctypes.c_float),
+                ("h_out", ctypes.c_void_p), ("ld_h", ctypes.c_int64), ("Xq", ctypes.c_void_p),
+                ("x_scale", ctypes.c_void_p)]
 
 
 class SQError(RuntimeError):
@@ -134,11 +156,21 @@ def _declare(L):
     L.sq_w8a8_gemm_plan.argtypes = [_I64, _I64, _I64, _I32, _I32, ctypes.POINTER(GemmPlanInfo)]
     L.sq_set_wait_limit.argtypes = [_I64]
     L.sq_set_wait_limit.restype = None
+    L.sq_moe_route_workspace_size.argtypes = [_I64, _I64, _I32]
+    L.sq_moe_route_workspace_size.restype = _SZ
+    L.sq_moe_route.argtypes = [_P, _I32, _I64, _I64, _I64, _I32, _I32, _P, _I32, _F32, _P, _P, _P,
+                               _P, _P, _P, _SZ, _P]
+    L.sq_w8a8_gemm_grouped.argtypes = [_P, _I64, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I32,
+                                       _P, _I64, _I32, _P]
+    L.sq_fp8_gemm_grouped.argtypes = L.sq_w8a8_gemm_grouped.argtypes
+    L.sq_block_norm_quant_per_token.argtypes = [ctypes.POINTER(BlockNormArgs), _P]
+    L.sq_block_norm_quant_per_token_fp8.argtypes = [ctypes.POINTER(BlockNormArgs), _P]
     for name in EXPORTS:
         f = getattr(L, name)
         if f.argtypes is None:  # every call passes 64-bit sizes: no implicit int conversion
             raise RuntimeError("no argument types declared for %s" % name)
-        if name not in ("sq_w8a8_gemm_workspace_size", "sq_status_string", "sq_set_wait_limit"):
+        if name not in ("sq_w8a8_gemm_workspace_size", "sq_status_string", "sq_set_wait_limit",
+                        "sq_moe_route_workspace_size"):
             f.restype = _I32
 
 
@@ -174,7 +206,7 @@ def _dtype_code(t: torch.Tensor) -> int:
 def _rows(t: torch.Tensor, name: str):
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1 and t.shape[0] > 0):
         raise ValueError("%s must be 2-D with unit column stride" % name)
     # a single row's stride is arbitrary (numpy / torch may report 0 for it)
     ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
@@ -617,6 +649,190 @@ def linear_w8a8(x: torch.Tensor, norm: int, gamma_folded, beta_folded, eps: floa
                                 _ptr(Xq_scratch), _ptr(xscale_scratch), _ptr(workspace), wsb,
                                 _stream(stream)), "sq_linear_w8a8")
     return out
+
+
+# ---- layers of experts -----------------------------------------------------
+
+class MoeRoute(NamedTuple):
+    """What :func:`moe_route` gives: see sq_moe_route in include/sq.h."""
+    weights: torch.Tensor    # [T, top_k] fp32
+    experts: torch.Tensor    # [T, top_k] int32, -1: none
+    offsets: torch.Tensor    # [E + 1] int32, expert e's rows are offsets[e] .. offsets[e + 1]
+    row_token: torch.Tensor  # [T * top_k] int32, the token of each row
+    token_row: torch.Tensor  # [T, top_k] int32, the row of each token's j-th expert, -1: none
+
+
+def _scope(device: torch.device, stream):
+    """The context of a call on tensors of ``device``: that device current, and
+    what the call allocates taken from the memory of the stream it runs on."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, device))
+        return torch.cuda.stream(stream)
+    if torch.cuda.current_device() == device.index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _dense(t: Optional[torch.Tensor], shape, dtype, device, name: str):
+    """A contiguous tensor of exactly this shape, type and device (or None)."""
+    if t is not None and (t.dtype != dtype or t.shape != shape or t.device != device
+                          or not t.is_contiguous()):
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s"
+                         % (name, dtype, list(shape), device))
+    return t
+
+
+def _out(t: Optional[torch.Tensor], shape, dtype, device, name: str):
+    """The caller's output tensor, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _dense(t, shape, dtype, device, name)
+
+
+def moe_route_workspace_size(T: int, E: int, top_k: int) -> int:
+    return int(lib().sq_moe_route_workspace_size(T, E, top_k))
+
+
+def moe_route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias=None,
+              renormalize: bool = True, scale: float = 1.0, weights=None, experts=None,
+              offsets=None, row_token=None, token_row=None, workspace=None,
+              stream=None) -> MoeRoute:
+    """The top_k experts of every token from the router's logits [T, E] (fp32 or
+    bf16), and the (token, expert) rows sorted by expert.  ``score``: "softmax"
+    or "sigmoid"; ``bias`` [E] (sigmoid only) is added for the choice alone."""
+    T, E, ld = _rows(logits, "logits")
+    dev = logits.device
+    if score not in MOE_SCORES:
+        raise ValueError("score must be one of %s" % sorted(MOE_SCORES))
+    if not 1 <= top_k <= E:
+        raise ValueError("top_k must be 1 .. %d (the experts), got %d" % (E, top_k))
+    f32, i32 = torch.float32, torch.int32
+    _dense(bias, (E,), f32, dev, "bias")
+    with _scope(dev, stream):
+        weights = _out(weights, (T, top_k), f32, dev, "weights")
+        experts = _out(experts, (T, top_k), i32, dev, "experts")
+        offsets = _out(offsets, (E + 1,), i32, dev, "offsets")
+        row_token = _out(row_token, (T * top_k,), i32, dev, "row_token")
+        token_row = _out(token_row, (T, top_k), i32, dev, "token_row")
+        need = moe_route_workspace_size(T, E, top_k)
+        if workspace is None and need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
+        _check(lib().sq_moe_route(_ptr(logits), _dtype_code(logits), T, E, ld, top_k,
+                                  MOE_SCORES[score], _ptr(bias), int(renormalize), scale,
+                                  _ptr(weights), _ptr(experts), _ptr(offsets), _ptr(row_token),
+                                  _ptr(token_row), _ptr(workspace), wsb, _stream(stream)),
+               "sq_moe_route")
+    return MoeRoute(weights, experts, offsets, row_token, token_row)
+
+
+def _gemm_grouped(call: str, code: torch.dtype, raw: str, Xq, Wq, x_scale, w_scale, offsets,
+                  row_token, epi, out, path_hint, stream):
+    if Xq.dim() != 2 or Wq.dim() != 3 or Wq.shape[2] != Xq.shape[1] or Xq.dtype != code \
+            or Wq.dtype != code or not Xq.is_contiguous() or not Wq.is_contiguous() \
+            or not Xq.is_cuda or Wq.device != Xq.device:
+        raise ValueError("Xq [X,K] and Wq [E,N,K] must be contiguous %s tensors on one CUDA "
+                         "device" % code)
+    X, K = Xq.shape
+    E, N, _ = Wq.shape
+    dev = Xq.device
+    if epi not in ("bf16", "bf16_relu", raw):
+        raise ValueError("epi must be bf16, bf16_relu or %s" % raw)
+    want = torch.bfloat16 if epi != raw else torch.int32 if raw == "i32" else torch.float32
+    R = X if row_token is None else row_token.numel()
+    _dense(offsets, (E + 1,), torch.int32, dev, "offsets")
+    _dense(row_token, (R,), torch.int32, dev, "row_token")
+    _dense(x_scale, (X,), torch.float32, dev, "x_scale")
+    _dense(w_scale, (E, N), torch.float32, dev, "w_scale")
+    with _scope(dev, stream):
+        if out is None:
+            out = torch.empty((R, N), dtype=want, device=dev)
+        elif (out.dim() != 2 or out.shape != (R, N) or out.dtype != want or out.device != dev
+              or (N > 1 and out.stride(1) != 1) or (R > 1 and out.stride(0) < N)):
+            raise ValueError("out must be a [R, N] = [%d, %d] %s tensor with unit column stride "
+                             "on the device of Xq" % (R, N, want))
+        ldo = out.stride(0) if R > 1 else max(N, 1)
+        _check(getattr(lib(), call)(_ptr(Xq), X, _ptr(Wq), _ptr(x_scale), _ptr(w_scale),
+                                    _ptr(offsets), _ptr(row_token), R, E, N, K, EPI[epi],
+                                    _ptr(out), ldo, path_hint, _stream(stream)), call)
+    return out
+
+
+def w8a8_gemm_grouped(Xq: torch.Tensor, Wq: torch.Tensor, x_scale: Optional[torch.Tensor],
+                      w_scale: Optional[torch.Tensor], offsets: torch.Tensor, row_token=None,
+                      epi: str = "bf16", out=None, path_hint: int = 0, stream=None
+                      ) -> torch.Tensor:
+    """Rows grouped by expert times each expert's weights: out[r] = row
+    ``row_token[r]`` (or r) of Xq [X, K] by Wq[e] ([E, N, K]) for offsets[e] <=
+    r < offsets[e + 1], dequantised to bf16 ("i32": the accumulator).  Rows of
+    ``out`` behind offsets[E] are left as they were."""
+    return _gemm_grouped("sq_w8a8_gemm_grouped", torch.int8, "i32", Xq, Wq, x_scale, w_scale,
+                         offsets, row_token, epi, out, path_hint, stream)
+
+
+def fp8_gemm_grouped(Xq8: torch.Tensor, Wq8: torch.Tensor, x_scale: Optional[torch.Tensor],
+                     w_scale: Optional[torch.Tensor], offsets: torch.Tensor, row_token=None,
+                     epi: str = "bf16", out=None, path_hint: int = 0, stream=None
+                     ) -> torch.Tensor:
+    """:func:`w8a8_gemm_grouped` on e4m3 bytes (uint8); "f32": the accumulator."""
+    return _gemm_grouped("sq_fp8_gemm_grouped", torch.uint8, "f32", Xq8, Wq8, x_scale, w_scale,
+                         offsets, row_token, epi, out, path_hint, stream)
+
+
+def block_norm_quant_per_token(x: torch.Tensor, residual: Optional[torch.Tensor] = None, *,
+                               token_row=None, weights=None, post_norm: int = NORM_NONE,
+                               post_gamma=None, post_beta=None, post_eps: float = 1e-5,
+                               gate=None, token_gate=None, residual_scale: float = 1.0,
+                               pre_norm: int = NORM_RMS, pre_gamma=None, pre_beta=None,
+                               pre_eps: float = 1e-5, fp8: bool = False, quant: bool = True,
+                               h_out=None, Xq=None, x_scale=None, stream=None):
+    """(h, Xq, x_scale) of the end of one block and the start of the next:
+    h = residual_scale * residual + post_norm(x) * gate * token_gate, codes of
+    pre_norm(h) per token.  With ``token_row`` and ``weights`` [M, top_k] x holds
+    the experts' rows [R, K] and each token's are summed first.  ``h_out`` may be
+    ``residual`` itself; without ``quant`` only h is computed (None, None)."""
+    R, K, ldx = _rows(x, "x")
+    dev, dt = x.device, x.dtype
+    a = BlockNormArgs()
+    a.dtype = _dtype_code(x)
+    M, top_k = R, 0
+    if (token_row is None) != (weights is None):
+        raise ValueError("token_row and weights go together")
+    if token_row is not None:
+        if token_row.dim() != 2:
+            raise ValueError("token_row must be [M, top_k]")
+        M, top_k = token_row.shape
+        a.token_row = _dense(token_row, (M, top_k), torch.int32, dev, "token_row").data_ptr()
+        a.weights = _dense(weights, (M, top_k), torch.float32, dev, "weights").data_ptr()
+    a.x, a.ldx, a.R, a.top_k, a.M, a.K = x.data_ptr(), ldx, R, top_k, M, K
+    for name, v, n in (("post_gamma", post_gamma, K), ("post_beta", post_beta, K),
+                       ("gate", gate, K), ("token_gate", token_gate, M),
+                       ("pre_gamma", pre_gamma, K), ("pre_beta", pre_beta, K)):
+        if v is not None:
+            setattr(a, name, _dense(v, (n,), torch.float32, dev, name).data_ptr())
+    a.post_norm, a.post_eps, a.pre_norm, a.pre_eps = post_norm, post_eps, pre_norm, pre_eps
+    for name, v in (("residual", residual), ("h_out", h_out)):
+        if v is not None and (v.shape != (M, K) or v.dtype != dt or v.device != dev):
+            raise ValueError("%s must be [%d, %d] %s on the device of x" % (name, M, K, dt))
+    if residual is not None:
+        a.residual, a.ld_res = residual.data_ptr(), _rows(residual, "residual")[2]
+    a.residual_scale = residual_scale
+    with _scope(dev, stream):
+        if h_out is None:
+            h_out = torch.empty((M, K), dtype=dt, device=dev)
+        a.h_out, a.ld_h = h_out.data_ptr(), _rows(h_out, "h_out")[2]
+        if quant:
+            Xq = _out(Xq, (M, K), torch.uint8 if fp8 else torch.int8, dev, "Xq")
+            x_scale = _out(x_scale, (M,), torch.float32, dev, "x_scale")
+            a.Xq, a.x_scale = Xq.data_ptr(), x_scale.data_ptr()
+        else:
+            Xq = x_scale = None
+        if M == 0:
+            return h_out, Xq, x_scale
+        call = "sq_block_norm_quant_per_token_fp8" if fp8 else "sq_block_norm_quant_per_token"
+        _check(getattr(lib(), call)(ctypes.byref(a), _stream(stream)), call)
+    return h_out, Xq, x_scale
 
 
 def get_device_error(stream=None) -> int:
