@@ -654,6 +654,8 @@ sq_status gemm_grouped(const void* Xq, int64_t X, const void* Wq, const float* x
   if (K > SQ_MAX_K) return SQ_ERR_OVERFLOW_RISK;
   // tensor-map coordinates and row numbers are 32-bit
   if (X > 0x7fffffff || R > 0x7fffffff || N > 0x7fffffff / E) return SQ_ERR_UNSUPPORTED;
+  // so are tile numbers: at most one tile per 16 rows (and expert) and 128 columns
+  if ((R / 16 + E + 1) * (N / 128 + 1) > 0x3fffffff) return SQ_ERR_UNSUPPORTED;
   const uintptr_t esz = epi == raw ? 4 : 2;
   if (K % 16 != 0 || !aligned16(Xq) || !aligned16(Wq) ||
       reinterpret_cast<uintptr_t>(out) % esz != 0 || !aligned4(x_scale) || !aligned4(w_scale) ||
@@ -662,8 +664,8 @@ sq_status gemm_grouped(const void* Xq, int64_t X, const void* Wq, const float* x
   int* err = device_error_word();
   if (!err) return SQ_ERR_CUDA;
   return from_cuda(launch_gemm_grouped(Xq, X, Wq, x_scale, w_scale, offsets, row_token, R, E, N, K,
-                                       epi, out, ldo, path_hint, g_wait_polls.load(), err, fp8,
-                                       as_stream(stream)));
+                                       epi, out, ldo, path_hint, sms_cached(), g_wait_polls.load(), err,
+                                       fp8, as_stream(stream)));
 }
 
 // Bytes [p, p + n) against [q, q + m).

@@ -63,21 +63,6 @@ constexpr int kSchedWarp = 6;
 // the previous grid has finished: 256 KB per SM, 38 MB over 148 SMs.
 constexpr int kPrefetchBlocks = 16;
 
-// Named barrier 1 joins the MMA-issuing warp and its scheduling warp once per
-// wait; the OR of the two warps' predicates tells both whether to stop.
-__device__ __forceinline__ bool sched_sync(bool stop) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 q, %1, 0;\n\t"
-      "bar.red.or.pred p, 1, 64, q;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r)
-      : "r"(stop ? 1u : 0u)
-      : "memory");
-  return r != 0;
-}
-
 template <int BN>
 struct Cfg {
   static constexpr int A_BYTES = BM * BK;
@@ -121,36 +106,6 @@ struct Params {
   // binary32 bits, for a following per-token requantisation (or null)
   float* row_absmax;
 };
-
-// Give-up point of a pipeline wait, in SM clock cycles (about 2 s at the
-// B200's 1.965 GHz maximum clock, longer at lower clocks).
-constexpr long long kWaitBudgetCycles = 4000000000LL;
-
-// Bounded wait on an mbarrier phase; `abort` may be null.  The first probe is
-// free of any timer read (the common case: the phase is already complete);
-// the budget is kept with the SM-local cycle counter, which is cheap to read
-// (the global nanosecond timer costs a few hundred cycles per read).
-__device__ bool wait_phase(uint32_t bar, uint32_t parity, int64_t polls, const volatile int* abort) {
-  if (mbar_try_wait(bar, parity)) return true;
-  if (polls > 0) {
-    for (int64_t i = 1; i < polls; ++i) {
-      if (mbar_try_wait(bar, parity)) return true;
-      if (abort && *abort) return false;
-    }
-    return false;
-  }
-  const long long t0 = clock64();
-  for (uint32_t i = 0;; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (abort && *abort) return false;
-    if ((i & 63u) == 63u && clock64() - t0 > kWaitBudgetCycles) return false;
-  }
-}
-
-__device__ __forceinline__ void fail(int* word, volatile int* abort) {
-  record_device_error(word, SQ_ERR_PIPELINE_TIMEOUT);
-  *abort = 1;
-}
 
 // Tile number -> (P block, Q block): bands of `group` P blocks sweep all Q
 // blocks before the next band starts, so a band's Q operand stays in L2.
@@ -1097,6 +1052,14 @@ bool make_map(CUtensorMap* map, const int8_t* ptr, int64_t rows, int64_t K, int 
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
+
+}  // namespace
+
+bool make_code_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t K, int box_rows) {
+  return make_map(map, static_cast<const int8_t*>(ptr), rows, K, box_rows);
+}
+
+namespace {
 
 template <int BN, bool kF8>
 cudaError_t launch_bn(const Params& prm, const CUtensorMap& mp, const CUtensorMap& mq, int grid,

@@ -1,10 +1,36 @@
 // grouped.cu -- the 8-bit GEMM of rows grouped by expert, each group with its
-// own weights, and the fused dequantising epilogue ("SmoothQuant, in depth" --
-// "Granularity": an INT32 accumulator, both scales in the epilogue).
+// own weights, and the fused dequantising epilogue, on the sm_100a tensor cores
+// (tcgen05 + tensor memory + TMA).  ("SmoothQuant, in depth" -- "Granularity":
+// an INT32 accumulator, both scales in the epilogue.)
+//
+// The group sizes are on the device and ragged, so the weights take the MMA's M
+// side -- full blocks of 128 (256 on a CTA pair) weight rows whatever the
+// groups are -- and the tokens its N side, whose width is set per tile in the
+// instruction descriptor: an expert with c rows runs ceil(c / QT) tiles of
+// equal width, rounded up to 16 (pairs: 32) rows, so a small or ragged group
+// costs MMA time and token loads for little more than its own rows.
+//   pair tiles   (prefill) 256 weight rows x up to 256 tokens on a CTA pair
+//                (cta_group::2), two accumulators in tensor memory;
+//   decode tiles 128 weight rows x up to 32 tokens per CTA, the weight stream's
+//                K range split over a cluster of up to 4 CTAs when there are too
+//                few tiles to fill the SMs; the partial sums meet through
+//                distributed shared memory, added in rank order by rank 0.
+// Every CTA first turns the offsets into a table of the non-empty experts and
+// their tiles; persistent CTAs then walk the flattened tiles, a weight block's
+// token tiles next to each other, so a weight byte comes from HBM once.
+// Tokens are gathered by TMA (tile::gather4: four rows at their own row
+// coordinates per instruction, a lane of the producer warp each), so sorting
+// the rows by expert never copies them.
+// Warp roles as in gemm.cu: 0 producer, 1 MMA issuer, 2-5 epilogue, 6 the
+// issuer's scheduler.  Every wait is bounded; one that runs out records
+// SQ_ERR_PIPELINE_TIMEOUT and the CTAs drain and return.
+#include <cuda.h>
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
+
+#include <atomic>
 
 #include "sq_device.cuh"
 #include "sq_launch.h"
@@ -12,96 +38,576 @@
 namespace sq {
 namespace {
 
-constexpr int TR = 32, TC = 64, TK = 64;  // rows, columns, K bytes of a step
+constexpr int BK = 128;      // K bytes per stage = one 128-byte swizzle atom row
+constexpr int UMMA_K = 32;   // K of one 8-bit MMA
+constexpr int kThreads = 224;
+constexpr int kSchedWarp = 6;
+constexpr int kMaxExperts = SQ_MOE_MAX_EXPERTS;
+constexpr int kBand = 16;    // token tiles of a band: their codes stay in L2 while it sweeps N
+constexpr int kBoxRows = 16; // rows of a token box where rows are contiguous
+
+template <bool kPair>
+struct Cfg {
+  static constexpr int QT = kPair ? 256 : 32;          // tokens of a tile at most
+  static constexpr int GRAIN = kPair ? 32 : 16;        // tile widths are multiples of this
+  static constexpr int PT = kPair ? 256 : 128;         // weight rows of a tile
+  static constexpr int Q_LOCAL = kPair ? QT / 2 : QT;  // token rows a CTA loads at most
+  static constexpr int A_BYTES = 128 * BK;
+  static constexpr int B_BYTES = Q_LOCAL * BK;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int STAGES = kPair ? 6 : 8;
+  static constexpr int TMEM_COLS = kPair ? 512 : 64;   // two accumulators
+  static constexpr int JOIN_SLOTS = kPair ? 0 : 3;     // partial sums of the other cluster ranks
+  static constexpr int JOIN_BYTES = 128 * QT * 4;      // [token][128 weight rows]
+  static constexpr int NUM_BARS = 2 * STAGES + 7;
+  static constexpr int TABLE = STAGES * STAGE_BYTES + JOIN_SLOTS * JOIN_BYTES;
+  static constexpr int BARS = TABLE + kMaxExperts * 16;
+  static constexpr int SMEM_BYTES = 1024 + BARS + 8 * NUM_BARS + 16;
+  static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
+  static_assert(STAGE_BYTES % 1024 == 0, "swizzle atoms need 1024-byte aligned stages");
+};
 
 struct GroupedParams {
-  const uint8_t* Xq;
-  const uint8_t* Wq;
   const float* x_scale;
   const float* w_scale;
   const int32_t* offsets;
   const int32_t* row_token;
-  int64_t X, R, N, K;
-  int E, epi;
   void* out;
   int64_t ldo;
+  int X, R, E, N, k_blocks, p_blocks, epi;
+  int split;            // CTAs of a cluster that share a tile's K range (decode tiles)
+  int64_t wait_polls;   // > 0: poll budget per wait; 0: ~2 s of SM clock cycles
+  int* error_word;
 };
 
-__device__ __forceinline__ float e4m3(uint8_t c) {
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
+// A non-empty expert: its rows are [begin, begin + count), its tiles the
+// flattened units up to unit_end.
+struct Entry {
+  int expert, begin, count, unit_end;
+};
+
+template <bool kPair>
+__device__ __forceinline__ int tiles_of(int count) {
+  return (count + Cfg<kPair>::QT - 1) / Cfg<kPair>::QT;
+}
+
+// The table, by one warp; returns the number of entries (in every lane).
+template <bool kPair>
+__device__ int build_table(const GroupedParams& p, Entry* table, int lane) {
+  int entries = 0, units = 0;
+  for (int e0 = 0; e0 < p.E; e0 += 32) {
+    const int e = e0 + lane;
+    int begin = 0, count = 0;
+    if (e < p.E) {
+      begin = min(max(__ldg(p.offsets + e), 0), p.R);
+      count = max(min(max(__ldg(p.offsets + e + 1), 0), p.R) - begin, 0);
+    }
+    const int mine = tiles_of<kPair>(count) * p.p_blocks;
+    int inc = mine;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+      const int u = __shfl_up_sync(~0u, inc, s);
+      if (lane >= s) inc += u;
+    }
+    const uint32_t active = __ballot_sync(~0u, count > 0);
+    if (count > 0)
+      table[entries + __popc(active & ((1u << lane) - 1u))] = Entry{e, begin, count, units + inc};
+    entries += __popc(active);
+    units += __shfl_sync(~0u, inc, 31);
+  }
+  return entries;
+}
+
+struct Tile {
+  int expert, pb, row0, rows, width;  // width: rows rounded up to the grain
+};
+
+// The tiles of one cluster, in order; every warp role walks the same sequence.
+template <bool kPair>
+struct Walk {
+  const Entry* table;
+  int entries, p_blocks, u, step, i, first;
+  __device__ __forceinline__ Walk(const GroupedParams& p, const Entry* t, int n, int id, int count)
+      : table(t), entries(n), p_blocks(p.p_blocks), u(id), step(count), i(0), first(0) {}
+  __device__ __forceinline__ bool next(Tile& t) {
+    if (i >= entries) return false;
+    Entry e = table[i];
+    while (u >= e.unit_end) {
+      first = e.unit_end;
+      if (++i >= entries) return false;
+      e = table[i];
+    }
+    const int q_tiles = tiles_of<kPair>(e.count);
+    const int grain = Cfg<kPair>::GRAIN;
+    const int width = ((e.count + q_tiles - 1) / q_tiles + grain - 1) / grain * grain;
+    // bands of token tiles sweep the weight blocks, a block's tiles together
+    const int idx = u - first;
+    const int band = idx / (kBand * p_blocks);
+    const int rem = idx - band * kBand * p_blocks;
+    const int size = min(kBand, q_tiles - band * kBand);
+    const int qb = band * kBand + rem % size;
+    t.expert = e.expert;
+    t.pb = rem / size;
+    t.row0 = e.begin + qb * width;
+    t.rows = min(width, e.count - qb * width);
+    t.width = (t.rows + grain - 1) / grain * grain;
+    u += step;
+    return true;
+  }
+};
+
+// The row of Xq a row of the grouped matrix reads, or -1.
+__device__ __forceinline__ int source_row(const GroupedParams& p, int r) {
+  if (!p.row_token) return r;
+  const int s = __ldg(p.row_token + r);
+  return s >= 0 && s < p.X ? s : -1;
 }
 
 template <bool kF8>
-__global__ void __launch_bounds__(256) grouped_simple_kernel(const GroupedParams p) {
-  __shared__ uint32_t xs[TR][TK / 4 + 1], ws[TC][TK / 4 + 1];
-  __shared__ int64_t src[TR];
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * TC;
-  const int e = blockIdx.y;
-  const int64_t begin = min(max(static_cast<int64_t>(p.offsets[e]), int64_t(0)), p.R);
-  const int64_t end = min(static_cast<int64_t>(p.offsets[e + 1]), p.R);
-  const int tc = threadIdx.x % 32, tr = threadIdx.x / 32;
-  for (int64_t r0 = begin; r0 < end; r0 += TR) {
-    __syncthreads();
-    if (threadIdx.x < TR) {
-      const int64_t r = r0 + threadIdx.x;
-      int64_t s = -1;
-      if (r < end) s = p.row_token ? p.row_token[r] : r;
-      src[threadIdx.x] = s >= 0 && s < p.X ? s : -1;
+__device__ __forceinline__ float acc_value(uint32_t r) {
+  if constexpr (kF8) return __uint_as_float(r);
+  else return __int2float_rn(static_cast<int>(r));
+}
+
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+template <bool kPair, bool kF8>
+__global__ void __launch_bounds__(kThreads, 1)
+    grouped_gemm_kernel(const __grid_constant__ CUtensorMap mapW,
+                        const __grid_constant__ CUtensorMap mapX, const GroupedParams prm) {
+  using C = Cfg<kPair>;
+  constexpr int STAGES = C::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_u32 = smem_u32(smem_raw);
+  const uint32_t base = (raw_u32 + 1023u) & ~1023u;
+  uint8_t* base_ptr = smem_raw + (base - raw_u32);
+  const uint32_t a_base = base;
+  const uint32_t b_base = base + STAGES * C::A_BYTES;
+  const uint32_t join_base = base + STAGES * C::STAGE_BYTES;
+  Entry* table = reinterpret_cast<Entry*>(base_ptr + C::TABLE);
+  const uint32_t bar_base = base + C::BARS;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + C::BARS + 8 * C::NUM_BARS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* entries_slot = reinterpret_cast<int*>(tmem_slot + 2);
+#define FULL_BAR(s) (bar_base + 8u * static_cast<uint32_t>(s))
+#define EMPTY_BAR(s) (bar_base + 8u * static_cast<uint32_t>(STAGES + (s)))
+#define TFULL_BAR(a) (bar_base + 8u * static_cast<uint32_t>(2 * STAGES + (a)))
+#define TEMPTY_BAR(a) (bar_base + 8u * static_cast<uint32_t>(2 * STAGES + 2 + (a)))
+#define DRAIN_BAR (bar_base + 8u * static_cast<uint32_t>(2 * STAGES + 4))
+#define JOIN_FULL_BAR (bar_base + 8u * static_cast<uint32_t>(2 * STAGES + 5))
+#define JOIN_EMPTY_BAR (bar_base + 8u * static_cast<uint32_t>(2 * STAGES + 6))
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int csize = kPair ? 2 : prm.split;  // CTAs of the cluster
+  const int rank = csize > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const bool issues = !kPair || rank == 0;  // this CTA's warp 1 issues MMAs
+  const int id = static_cast<int>(blockIdx.x) / csize;
+  const int clusters = static_cast<int>(gridDim.x) / csize;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(FULL_BAR(s), 1);
+      mbar_init(EMPTY_BAR(s), 1);
     }
-    int ai[TR / 8][2] = {};
-    float af[TR / 8][2] = {};
-    for (int64_t k0 = 0; k0 < p.K; k0 += TK) {
-      __syncthreads();
-      for (int i = threadIdx.x; i < TR * TK / 4; i += 256) {
-        const int r = i / (TK / 4), c = i % (TK / 4);
-        uint32_t v = 0;
-        if (src[r] >= 0 && k0 + 4 * c < p.K)
-          v = *reinterpret_cast<const uint32_t*>(p.Xq + src[r] * p.K + k0 + 4 * c);
-        xs[r][c] = v;
-      }
-      for (int i = threadIdx.x; i < TC * TK / 4; i += 256) {
-        const int n = i / (TK / 4), c = i % (TK / 4);
-        uint32_t v = 0;
-        if (n0 + n < p.N && k0 + 4 * c < p.K)
-          v = *reinterpret_cast<const uint32_t*>(p.Wq + (e * p.N + n0 + n) * p.K + k0 + 4 * c);
-        ws[n][c] = v;
-      }
-      __syncthreads();
-      for (int c = 0; c < TK / 4; ++c) {
-#pragma unroll
-        for (int i = 0; i < TR / 8; ++i)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint32_t x = xs[tr + 8 * i][c], w = ws[tc + 32 * j][c];
-            if constexpr (kF8) {
-#pragma unroll
-              for (int b = 0; b < 4; ++b)
-                af[i][j] = fmaf(e4m3((x >> (8 * b)) & 0xff), e4m3((w >> (8 * b)) & 0xff), af[i][j]);
-            } else {
-              ai[i][j] = __dp4a(static_cast<int>(x), static_cast<int>(w), ai[i][j]);
-            }
-          }
-      }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(TFULL_BAR(a), 1);
+      mbar_init(TEMPTY_BAR(a), kPair ? 8 : 4);
     }
+    mbar_init(DRAIN_BAR, 1);
+    mbar_init(JOIN_FULL_BAR, csize > 1 ? 4 * (csize - 1) : 1);  // every warp of the other ranks
+    mbar_init(JOIN_EMPTY_BAR, 4);                               // rank 0's epilogue warps
+    *abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&mapW);
+    tma_prefetch_desc(&mapX);
+  }
+  if (warp == 1) {
+    if constexpr (kPair) {
+      tmem_alloc_pair(smem_u32(tmem_slot), C::TMEM_COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
+      tmem_relinquish();
+    }
+  }
+  // programmatic launch: the next kernel may be scheduled; this one reads and
+  // writes global memory only after the previous grid has completed
+  if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (warp == 0) {
+    const int n = build_table<kPair>(prm, table, lane);
+    if (lane == 0) *entries_slot = n;
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (csize > 1) cluster_sync_all();  // every CTA's barriers exist before any cross-CTA signal
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int entries = *entries_slot;
+  const int64_t polls = prm.wait_polls;
+  // the K blocks of this CTA
+  const int kb0 = kPair ? 0 : static_cast<int>(static_cast<int64_t>(rank) * prm.k_blocks / csize);
+  const int kb1 = kPair ? prm.k_blocks
+                        : static_cast<int>(static_cast<int64_t>(rank + 1) * prm.k_blocks / csize);
+  Walk<kPair> walk(prm, table, entries, id, clusters);
+  Tile t;
+
+  // a wait ran out: stop every CTA of the cluster
+  auto give_up = [&]() {
+    fail(prm.error_word, abort_flag);
+    for (int c = 0; c < csize; ++c)
+      if (c != rank) st_cluster_u32(map_to_cta(smem_u32(const_cast<int*>(abort_flag)), c), 1u);
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    while (ok && walk.next(t)) {
+      const int local = kPair ? t.width >> 1 : t.width;  // token rows this CTA loads
+      const int j0 = kPair ? rank * local : 0;
+      const int w_row = t.expert * prm.N + t.pb * C::PT + (kPair ? rank * 128 : 0);
+      int src[4] = {0, 0, 0, 0};
+      if (prm.row_token) {
+        // a row past the tile, or of no token, loads token 0: its column is
+        // dropped, or zeroed, by the epilogue
 #pragma unroll
-    for (int i = 0; i < TR / 8; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int64_t r = r0 + tr + 8 * i, n = n0 + tc + 32 * j;
-        if (r >= end || n >= p.N) continue;
-        const int64_t o = r * p.ldo + n, s = src[tr + 8 * i];
-        if (p.epi == SQ_EPI_I32_RAW) {
-          static_cast<int32_t*>(p.out)[o] = ai[i][j];
-        } else if (p.epi == SQ_EPI_F32_RAW) {
-          static_cast<float*>(p.out)[o] = af[i][j];
-        } else {
-          const float acc = kF8 ? af[i][j] : __int2float_rn(ai[i][j]);
-          float t = __fmul_rn(__fmul_rn(acc, s >= 0 ? p.x_scale[s] : 0.0f), p.w_scale[e * p.N + n]);
-          if (p.epi == SQ_EPI_BF16_RELU) t = t > 0.0f ? t : 0.0f;
-          static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(t);
+        for (int i = 0; i < 4; ++i) {
+          const int j = j0 + 4 * lane + i;
+          if (4 * lane < local && j < t.rows) src[i] = max(source_row(prm, t.row0 + j), 0);
         }
       }
+      for (int kb = kb0; kb < kb1; ++kb) {
+        bool w = false;
+        if (lane == 0) w = wait_phase(EMPTY_BAR(stage), phase ^ 1u, polls, abort_flag);
+        w = __shfl_sync(~0u, w, 0);
+        if (!w) {
+          if (lane == 0) give_up();
+          ok = false;
+          break;
+        }
+        const uint32_t sa = a_base + stage * C::A_BYTES, sb = b_base + stage * C::B_BYTES;
+        // a pair's loads complete on the leader's barrier
+        const uint32_t fb = kPair && rank ? map_to_cta(FULL_BAR(stage), 0) : FULL_BAR(stage);
+        if (lane == 0) {
+          const uint32_t bytes = C::A_BYTES + local * BK;
+          if (issues) mbar_arrive_expect_tx(FULL_BAR(stage), kPair ? 2 * bytes : bytes);
+          if constexpr (kPair) tma_load_2d_pair(sa, &mapW, fb, kb * BK, w_row);
+          else tma_load_2d(sa, &mapW, fb, kb * BK, w_row);
+        }
+        __syncwarp();
+        if (prm.row_token) {
+          if (4 * lane < local) {
+            if constexpr (kPair) tma_gather4_pair(sb + lane * 4 * BK, &mapX, fb, kb * BK, src);
+            else tma_gather4(sb + lane * 4 * BK, &mapX, fb, kb * BK, src);
+          }
+        } else if (kBoxRows * lane < local) {
+          const int row = t.row0 + j0 + kBoxRows * lane;
+          if constexpr (kPair) tma_load_2d_pair(sb + lane * kBoxRows * BK, &mapX, fb, kb * BK, row);
+          else tma_load_2d(sb + lane * kBoxRows * BK, &mapX, fb, kb * BK, row);
+        }
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (issues) {
+      int stage = 0;
+      int acc = 0;
+      bool ok = true;
+      while (ok && walk.next(t)) {
+        const uint32_t idesc = kF8 ? idesc_f8(C::PT, t.width) : idesc_i8(C::PT, t.width);
+        if (sched_sync(false)) break;  // the scheduler saw this accumulator free (or gave up)
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * C::QT);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (sched_sync(false)) {  // the scheduler saw this stage land (or gave up)
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t sa = a_base + stage * C::A_BYTES;
+            const uint32_t sb = b_base + stage * C::B_BYTES;
+#pragma unroll
+            for (int kk = 0; kk < BK / UMMA_K; ++kk) {
+              const uint64_t da = smem_desc_k_sw128(sa + kk * UMMA_K);
+              const uint64_t db = smem_desc_k_sw128(sb + kk * UMMA_K);
+              const uint32_t add = (kb > kb0 || kk > 0) ? 1u : 0u;
+              if constexpr (kPair && kF8) mma_f8_pair(d_tmem, da, db, idesc, add);
+              else if constexpr (kPair) mma_i8_pair(d_tmem, da, db, idesc, add);
+              else if constexpr (kF8) mma_f8(d_tmem, da, db, idesc, add);
+              else mma_i8(d_tmem, da, db, idesc, add);
+            }
+            if constexpr (kPair) {
+              mma_commit_pair(EMPTY_BAR(stage));
+              mma_commit_pair(map_to_cta(EMPTY_BAR(stage), 1));
+            } else {
+              mma_commit(EMPTY_BAR(stage));
+            }
+          }
+          __syncwarp();
+          if (++stage == STAGES) stage = 0;
+        }
+        if (!ok) break;
+        if (lane == 0) {
+          if constexpr (kPair) {
+            mma_commit_pair(TFULL_BAR(acc));
+            mma_commit_pair(map_to_cta(TFULL_BAR(acc), 1));
+          } else {
+            mma_commit(TFULL_BAR(acc));
+          }
+        }
+        __syncwarp();
+        acc ^= 1;
+      }
+      if (lane == 0) {
+        // every MMA issued by this thread completes before tensor memory is freed
+        if constexpr (kPair) mma_commit_pair(DRAIN_BAR);
+        else mma_commit(DRAIN_BAR);
+        wait_phase(DRAIN_BAR, 0, 0, nullptr);
+      }
+      __syncwarp();
+    }
+  } else if (warp == kSchedWarp) {
+    // ------------------------------------------------------------ MMA scheduler
+    if (issues) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      bool ok = true;
+      while (ok && walk.next(t)) {
+        bool w = false;
+        if (lane == 0) w = wait_phase(TEMPTY_BAR(acc), acc_phase ^ 1u, polls, abort_flag);
+        w = __shfl_sync(~0u, w, 0);
+        if (!w && lane == 0) give_up();
+        if (sched_sync(!w)) break;
+        for (int kb = kb0; kb < kb1; ++kb) {
+          w = false;
+          if (lane == 0) w = wait_phase(FULL_BAR(stage), phase, polls, abort_flag);
+          w = __shfl_sync(~0u, w, 0);
+          if (!w && lane == 0) give_up();
+          if (sched_sync(!w)) {
+            ok = false;
+            break;
+          }
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int quarter = warp & 3;  // tensor-memory lanes this warp may access
+    const int p_local = quarter * 32 + lane;
+    const bool raw = prm.epi == SQ_EPI_I32_RAW || prm.epi == SQ_EPI_F32_RAW;
+    const bool relu = prm.epi == SQ_EPI_BF16_RELU;
+    int acc = 0;
+    uint32_t acc_phase = 0, join_phase = 0;
+    while (walk.next(t)) {
+      const int n = t.pb * C::PT + (kPair ? rank * 128 : 0) + p_local;  // output column
+      const bool n_in = n < prm.N;
+      float ws = 0.0f;
+      if (!raw && n_in && (kPair || rank == 0))
+        ws = __ldg(prm.w_scale + static_cast<int64_t>(t.expert) * prm.N + n);
+      bool w = false;
+      if (lane == 0) w = wait_phase(TFULL_BAR(acc), acc_phase, polls, abort_flag);
+      w = __shfl_sync(~0u, w, 0);
+      if (!w) {
+        if (lane == 0) give_up();
+        break;
+      }
+      tc_fence_after();
+      const uint32_t trow = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
+                            static_cast<uint32_t>(acc * C::QT);
+      bool stop = false;
+#pragma unroll 1
+      for (int c = 0; c < t.rows; c += 32) {
+        uint32_t r[32];
+        __syncwarp();
+        tmem_ld_32x32b_x32(trow + static_cast<uint32_t>(c), r);
+        // lane j holds what column c + j needs
+        const int row = t.row0 + c + lane;
+        int s = -1;
+        if (c + lane < t.rows) s = source_row(prm, row);
+        const float xs_l = !raw && s >= 0 ? __ldg(prm.x_scale + s) : 0.0f;
+        const uint32_t zero = __ballot_sync(~0u, s < 0);
+        tmem_wait_ld();
+        if constexpr (!kPair) {
+          if (csize > 1) {  // QT = 32: one chunk per tile
+            if (rank > 0) {
+              // partial sums to rank 0's slot, once it has read the last ones
+              if (lane == 0) w = wait_phase(JOIN_EMPTY_BAR, join_phase ^ 1u, polls, abort_flag);
+              w = __shfl_sync(~0u, w, 0);
+              if (!w) {
+                if (lane == 0) give_up();
+                stop = true;
+                break;
+              }
+              const uint32_t dst = map_to_cta(
+                  join_base + (rank - 1) * C::JOIN_BYTES + p_local * 4, 0);
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (j < t.rows) st_cluster_u32(dst + j * 512, r[j]);
+              asm volatile("fence.acq_rel.cluster;" ::: "memory");
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cluster(map_to_cta(JOIN_FULL_BAR, 0));
+            } else {
+              if (lane == 0) w = wait_phase(JOIN_FULL_BAR, join_phase, polls, abort_flag);
+              w = __shfl_sync(~0u, w, 0);
+              if (!w) {
+                if (lane == 0) give_up();
+                stop = true;
+                break;
+              }
+              mbar_try_wait_cluster(JOIN_FULL_BAR, join_phase);  // complete: acquires the stores
+              for (int o = 0; o < csize - 1; ++o) {
+                const uint32_t* src = reinterpret_cast<const uint32_t*>(
+                    base_ptr + (join_base - base) + o * C::JOIN_BYTES) + p_local;
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (j < t.rows) {
+                    const uint32_t v = src[j * 128];
+                    if constexpr (kF8)
+                      r[j] = __float_as_uint(__fadd_rn(__uint_as_float(r[j]), __uint_as_float(v)));
+                    else
+                      r[j] += v;
+                  }
+              }
+              __syncwarp();
+              if (lane == 0)
+                for (int o = 1; o < csize; ++o) mbar_arrive_cluster(map_to_cta(JOIN_EMPTY_BAR, o));
+            }
+            join_phase ^= 1u;
+            if (rank > 0) continue;
+          }
+        }
+        if (raw) {
+          uint32_t* dst = static_cast<uint32_t*>(prm.out) + static_cast<int64_t>(t.row0 + c) * prm.ldo + n;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            if (c + j < t.rows && n_in) *dst = (zero >> j) & 1u ? 0u : r[j];
+            dst += prm.ldo;
+          }
+        } else {
+          __nv_bfloat16* dst =
+              static_cast<__nv_bfloat16*>(prm.out) + static_cast<int64_t>(t.row0 + c) * prm.ldo + n;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float xs = __shfl_sync(~0u, xs_l, j);
+            float v = __fmul_rn(__fmul_rn(acc_value<kF8>(r[j]), xs), ws);
+            if ((zero >> j) & 1u) v = 0.0f;
+            if (relu) v = v > 0.0f ? v : 0.0f;  // -0 (a zero scale) becomes +0
+            if (c + j < t.rows && n_in) *dst = __float2bfloat16_rn(v);
+            dst += prm.ldo;
+          }
+        }
+      }
+      if (stop) break;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (kPair && rank) mbar_arrive_cluster(map_to_cta(TEMPTY_BAR(acc), 0));
+        else mbar_arrive(TEMPTY_BAR(acc));
+      }
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
+    }
   }
+  __syncthreads();
+  if (csize > 1) cluster_sync_all();  // no MMA, load signal or remote store is pending
+  if (*abort_flag) {
+    // after an abort some loads may still be in flight, and the barriers that
+    // would tell may never complete: about 20 ms, thousands of times a load's
+    // latency, pass before the shared memory is given back
+    const long long t0 = clock64();
+    while (clock64() - t0 < 40000000LL) {
+    }
+  }
+  __syncthreads();
+  if (csize > 1) cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    if constexpr (kPair) tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+    else tmem_dealloc(tmem_base, C::TMEM_COLS);
+  }
+#undef FULL_BAR
+#undef EMPTY_BAR
+#undef TFULL_BAR
+#undef TEMPTY_BAR
+#undef DRAIN_BAR
+#undef JOIN_FULL_BAR
+#undef JOIN_EMPTY_BAR
+}
+
+// Experts that get at least one of R rows, at even popularity.
+double active_experts(int64_t E, int64_t R) {
+  if (E <= 1) return 1.0;
+  return static_cast<double>(E) *
+         -expm1(static_cast<double>(R) * log1p(-1.0 / static_cast<double>(E)));
+}
+
+template <bool kPair, bool kF8>
+cudaError_t launch(const CUtensorMap& mw, const CUtensorMap& mx, const GroupedParams& prm,
+                   int64_t max_units, int sms, cudaStream_t st) {
+  using C = Cfg<kPair>;
+  auto kern = grouped_gemm_kernel<kPair, kF8>;
+  cudaError_t e = launch_cache().ensure_smem(reinterpret_cast<const void*>(kern), C::SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  const int csize = kPair ? 2 : prm.split;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(csize);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::SMEM_BYTES;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = csize > 1 ? 2 : 1;
+  int64_t clusters = sms / csize;
+  if (csize > 1) {
+    // as many clusters as the device holds at once, asked once per device and size
+    static std::atomic<int> held[64][5];
+    const int dev = LaunchCache::device();
+    int n = dev >= 0 && dev < 64 ? held[dev][csize].load() : 0;
+    if (n == 0) {
+      cfg.gridDim = dim3(static_cast<unsigned>(clusters * csize));
+      if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0)
+        n = static_cast<int>(clusters);
+      if (dev >= 0 && dev < 64) held[dev][csize].store(n);
+    }
+    if (n < clusters) clusters = n;
+  }
+  if (max_units < clusters) clusters = max_units;
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters * csize));
+  e = cudaLaunchKernelEx(&cfg, kern, mw, mx, prm);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
@@ -110,15 +616,47 @@ cudaError_t launch_gemm_grouped(const void* Xq, int64_t X, const void* Wq, const
                                 const float* w_scale, const int32_t* offsets,
                                 const int32_t* row_token, int64_t R, int64_t E, int64_t N,
                                 int64_t K, int epi, void* out, int64_t ldo, int path_hint,
-                                int64_t wait_polls, int* error_word, bool fp8, cudaStream_t st) {
-  GroupedParams p{static_cast<const uint8_t*>(Xq), static_cast<const uint8_t*>(Wq), x_scale, w_scale,
-                  offsets, row_token, X, R, N, K, static_cast<int>(E), epi, out, ldo};
-  const dim3 grid(static_cast<unsigned>((N + TC - 1) / TC), static_cast<unsigned>(E));
-  if (fp8)
-    grouped_simple_kernel<true><<<grid, 256, 0, st>>>(p);
-  else
-    grouped_simple_kernel<false><<<grid, 256, 0, st>>>(p);
-  return cudaGetLastError();
+                                int num_sms, int64_t wait_polls, int* error_word, bool fp8,
+                                cudaStream_t st) {
+  const int sms = num_sms > 0 ? num_sms : 148;
+  // decode tiles while an expert has few rows: they keep twice as many weight
+  // blocks in flight; past 32 rows an expert's weights would be read again for
+  // every 32
+  const bool pair = path_hint == 1 || (path_hint == 0 && R > 24 * E);
+  GroupedParams p{};
+  p.x_scale = x_scale;
+  p.w_scale = w_scale;
+  p.offsets = offsets;
+  p.row_token = row_token;
+  p.out = out;
+  p.ldo = ldo;
+  p.X = static_cast<int>(X);
+  p.R = static_cast<int>(R);
+  p.E = static_cast<int>(E);
+  p.N = static_cast<int>(N);
+  p.k_blocks = static_cast<int>((K + BK - 1) / BK);
+  const int pt = pair ? 256 : 128, qt = pair ? 256 : 32;
+  p.p_blocks = static_cast<int>((N + pt - 1) / pt);
+  p.epi = epi;
+  p.split = 1;
+  p.wait_polls = wait_polls;
+  p.error_word = error_word;
+  const int64_t max_units = ((R + qt - 1) / qt + (E < R ? E : R)) * p.p_blocks;
+  if (max_units > 0x3fffffff) return cudaErrorInvalidValue;
+  if (!pair) {
+    // enough clusters to fill the SMs, by the tiles to be expected
+    const double tiles = active_experts(E, R) * p.p_blocks;
+    while (p.split < 4 && tiles * p.split < 0.75 * sms && 2 * p.split <= p.k_blocks) p.split *= 2;
+  }
+  CUtensorMap mw, mx;
+  if (!make_code_map(&mw, Wq, E * N, K, 128) ||
+      !make_code_map(&mx, Xq, X, K, row_token ? 1 : kBoxRows))
+    return cudaErrorInvalidValue;
+  if (pair)
+    return fp8 ? launch<true, true>(mw, mx, p, max_units, sms, st)
+               : launch<true, false>(mw, mx, p, max_units, sms, st);
+  return fp8 ? launch<false, true>(mw, mx, p, max_units, sms, st)
+             : launch<false, false>(mw, mx, p, max_units, sms, st);
 }
 
 }  // namespace sq

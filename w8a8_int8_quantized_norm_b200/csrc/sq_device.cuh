@@ -81,6 +81,18 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+// Four rows of a row-major matrix (the map's box is one row of 128 bytes), each
+// at its own row coordinate, into four consecutive rows of shared memory.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                            int32_t c0, const int (&row)[4]) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(row[0]), "r"(row[1]),
+      "r"(row[2]), "r"(row[3])
+      : "memory");
+}
+
 // Bring a tile of a tensor map into L2 only (no shared memory, no barrier):
 // a hint, coherent with any later write (L2 is where global memory is kept
 // coherent), so it may be issued before the data's producer has finished.
@@ -219,6 +231,17 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
+__device__ __forceinline__ void tma_gather4_pair(uint32_t dst, const CUtensorMap* map,
+                                                 uint32_t bar_cluster, int32_t c0,
+                                                 const int (&row)[4]) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      ".cta_group::2 [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(c0), "r"(row[0]), "r"(row[1]),
+      "r"(row[2]), "r"(row[3])
+      : "memory");
+}
+
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem),
                "r"(ncols)
@@ -261,6 +284,55 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar_cluster) {
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
           bar_cluster)
       : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// bounded pipeline waits, and the handoff of the GEMMs' MMA-issuing warp
+// ---------------------------------------------------------------------------
+// Give-up point of a pipeline wait, in SM clock cycles (about 2 s at the
+// B200's 1.965 GHz maximum clock, longer at lower clocks).
+constexpr long long kWaitBudgetCycles = 4000000000LL;
+
+// Bounded wait on an mbarrier phase; `abort` may be null.  The first probe is
+// free of any timer read (the common case: the phase is already complete);
+// the budget is kept with the SM-local cycle counter, which is cheap to read
+// (the global nanosecond timer costs a few hundred cycles per read).
+inline __device__ bool wait_phase(uint32_t bar, uint32_t parity, int64_t polls,
+                                  const volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  if (polls > 0) {
+    for (int64_t i = 1; i < polls; ++i) {
+      if (mbar_try_wait(bar, parity)) return true;
+      if (abort && *abort) return false;
+    }
+    return false;
+  }
+  const long long t0 = clock64();
+  for (uint32_t i = 0;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (abort && *abort) return false;
+    if ((i & 63u) == 63u && clock64() - t0 > kWaitBudgetCycles) return false;
+  }
+}
+
+__device__ __forceinline__ void fail(int* word, volatile int* abort) {
+  record_device_error(word, SQ_ERR_PIPELINE_TIMEOUT);
+  *abort = 1;
+}
+
+// Named barrier 1 joins the MMA-issuing warp and its scheduling warp once per
+// wait; the OR of the two warps' predicates tells both whether to stop.
+__device__ __forceinline__ bool sched_sync(bool stop) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "bar.red.or.pred p, 1, 64, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(stop ? 1u : 0u)
+      : "memory");
+  return r != 0;
 }
 
 // Shared-memory matrix descriptor of a K-major operand tile stored in the

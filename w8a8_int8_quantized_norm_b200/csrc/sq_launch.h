@@ -2,6 +2,7 @@
 // public surface is include/sq.h).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -145,7 +146,8 @@ cudaError_t launch_gemm_grouped(const void* Xq, int64_t X, const void* Wq, const
                                 const float* w_scale, const int32_t* offsets,
                                 const int32_t* row_token, int64_t R, int64_t E, int64_t N,
                                 int64_t K, int epi, void* out, int64_t ldo, int path_hint,
-                                int64_t wait_polls, int* error_word, bool fp8, cudaStream_t st);
+                                int num_sms, int64_t wait_polls, int* error_word, bool fp8,
+                                cudaStream_t st);
 
 // blocknorm.cu (the end of one block and the start of the next)
 cudaError_t launch_block_norm(const sq_block_norm_args& a, bool fp8, cudaStream_t st);
@@ -168,6 +170,9 @@ cudaError_t launch_gemm(const GemmPlan& plan, const int8_t* Xq, const int8_t* Wq
                         int num_sms, int64_t wait_polls, int* error_word, cudaStream_t st,
                         float* row_absmax = nullptr, bool fp8 = false);
 int num_sms_current_device();
+// Tensor map of a K-major matrix of 8-bit codes [rows, K]: boxes of box_rows x
+// 128 bytes, 128-byte swizzle, zeros outside the matrix.
+bool make_code_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t K, int box_rows);
 // The dequantising epilogue of an INT32 accumulator matrix acc [M, N]
 // (stride lda): out = bf16(fl32(fl32(fl32(acc) x_scale[m]) w_scale[n])), ReLU
 // for SQ_EPI_BF16_RELU.
