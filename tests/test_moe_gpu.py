@@ -213,6 +213,14 @@ def test_grouped_shapes(N, K, fp8, path):
 
 
 @pytest.mark.parametrize("path", [1, 2])
+@pytest.mark.parametrize("fp8", [False, True], ids=["int8", "fp8"])
+@pytest.mark.parametrize("gather", [None, 300])
+def test_grouped_many_tiles_per_cta(gather, fp8, path):
+    """Persistent CTAs run several tiles of different widths one after another."""
+    _check_grouped([1040, 300, 0, 17, 1, 600, 33], 4000, 1040, fp8, gather=gather, path=path)
+
+
+@pytest.mark.parametrize("path", [1, 2])
 @pytest.mark.parametrize("epi", ["bf16_relu", "raw"])
 @pytest.mark.parametrize("fp8", [False, True], ids=["int8", "fp8"])
 def test_grouped_epilogues(epi, fp8, path):

@@ -19,10 +19,9 @@
 // their tiles; persistent CTAs then walk the flattened tiles, a weight block's
 // token tiles next to each other, so a weight byte comes from HBM once.
 // Tokens are gathered by TMA (tile::gather4: four rows at their own row
-// coordinates per instruction, a lane of the producer warp each), so sorting
-// the rows by expert never copies them.
+// coordinates per instruction), so sorting the rows by expert never copies them.
 // Warp roles as in gemm.cu: 0 producer, 1 MMA issuer, 2-5 epilogue, 6 the
-// issuer's scheduler.  Every wait is bounded; one that runs out records
+// issuer's scheduler; 7-10 gather tokens.  Every wait is bounded; one that runs out records
 // SQ_ERR_PIPELINE_TIMEOUT and the CTAs drain and return.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -40,16 +39,19 @@ namespace {
 
 constexpr int BK = 128;      // K bytes per stage = one 128-byte swizzle atom row
 constexpr int UMMA_K = 32;   // K of one 8-bit MMA
-constexpr int kThreads = 224;
 constexpr int kSchedWarp = 6;
+constexpr int kGatherWarp = 7;   // first of the warps that gather tokens
+constexpr int kGatherWarps = 4;
+constexpr int kThreads = 32 * (kGatherWarp + kGatherWarps);
 constexpr int kMaxExperts = SQ_MOE_MAX_EXPERTS;
 constexpr int kBand = 16;    // token tiles of a band: their codes stay in L2 while it sweeps N
-constexpr int kBoxRows = 16; // rows of a token box where rows are contiguous
+constexpr int kBoxes = 4;    // token boxes of 128, 64, 32 and 16 contiguous rows
 
 template <bool kPair>
 struct Cfg {
   static constexpr int QT = kPair ? 256 : 32;          // tokens of a tile at most
   static constexpr int GRAIN = kPair ? 32 : 16;        // tile widths are multiples of this
+  static constexpr int WIDTH_BITS = kPair ? 3 : 1;     // of width / GRAIN - 1
   static constexpr int PT = kPair ? 256 : 128;         // weight rows of a tile
   static constexpr int Q_LOCAL = kPair ? QT / 2 : QT;  // token rows a CTA loads at most
   static constexpr int A_BYTES = 128 * BK;
@@ -63,8 +65,17 @@ struct Cfg {
   static constexpr int TABLE = STAGES * STAGE_BYTES + JOIN_SLOTS * JOIN_BYTES;
   static constexpr int BARS = TABLE + kMaxExperts * 16;
   static constexpr int SMEM_BYTES = 1024 + BARS + 8 * NUM_BARS + 16;
+  static constexpr int GATHER = Q_LOCAL / kGatherWarps;  // rows a gather warp loads at most
+  static_assert(GATHER <= 32 && GATHER % 4 == 0, "a lane finds one row's token");
+  static_assert((kPair ? GRAIN / 2 : GRAIN) % (4 * kGatherWarps) == 0, "a gather4 per warp");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
+  static_assert(QT == GRAIN << WIDTH_BITS, "a tile's width in WIDTH_BITS bits");
   static_assert(STAGE_BYTES % 1024 == 0, "swizzle atoms need 1024-byte aligned stages");
+};
+
+// Token maps: [0] gathers (boxes of one row) or [0 .. kBoxes) contiguous boxes.
+struct TokenMaps {
+  CUtensorMap m[kBoxes];
 };
 
 struct GroupedParams {
@@ -129,13 +140,20 @@ struct Walk {
   int entries, p_blocks, u, step, i, first;
   __device__ __forceinline__ Walk(const GroupedParams& p, const Entry* t, int n, int id, int count)
       : table(t), entries(n), p_blocks(p.p_blocks), u(id), step(count), i(0), first(0) {}
+  // Called by whole warps; the shuffles make what is read uniform, so that TMA
+  // coordinates stay in uniform registers.
+  __device__ __forceinline__ Entry entry(int k) const {
+    const Entry e = table[k];
+    return Entry{__shfl_sync(~0u, e.expert, 0), __shfl_sync(~0u, e.begin, 0),
+                 __shfl_sync(~0u, e.count, 0), __shfl_sync(~0u, e.unit_end, 0)};
+  }
   __device__ __forceinline__ bool next(Tile& t) {
     if (i >= entries) return false;
-    Entry e = table[i];
+    Entry e = entry(i);
     while (u >= e.unit_end) {
       first = e.unit_end;
       if (++i >= entries) return false;
-      e = table[i];
+      e = entry(i);
     }
     const int q_tiles = tiles_of<kPair>(e.count);
     const int grain = Cfg<kPair>::GRAIN;
@@ -184,7 +202,7 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
 template <bool kPair, bool kF8>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_gemm_kernel(const __grid_constant__ CUtensorMap mapW,
-                        const __grid_constant__ CUtensorMap mapX, const GroupedParams prm) {
+                        const __grid_constant__ TokenMaps mapX, const GroupedParams prm) {
   using C = Cfg<kPair>;
   constexpr int STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
@@ -207,9 +225,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #define JOIN_FULL_BAR (bar_base + 8u * static_cast<uint32_t>(2 * STAGES + 5))
 #define JOIN_EMPTY_BAR (bar_base + 8u * static_cast<uint32_t>(2 * STAGES + 6))
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(~0u, static_cast<int>(threadIdx.x) >> 5, 0);
+  const int lane = threadIdx.x & 31;
   const int csize = kPair ? 2 : prm.split;  // CTAs of the cluster
-  const int rank = csize > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int rank = csize > 1 ? __shfl_sync(~0u, static_cast<int>(cluster_ctarank()), 0) : 0;
   const bool issues = !kPair || rank == 0;  // this CTA's warp 1 issues MMAs
   const int id = static_cast<int>(blockIdx.x) / csize;
   const int clusters = static_cast<int>(gridDim.x) / csize;
@@ -231,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&mapW);
-    tma_prefetch_desc(&mapX);
+    tma_prefetch_desc(&mapX.m[0]);
   }
   if (warp == 1) {
     if constexpr (kPair) {
@@ -254,8 +273,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (csize > 1) cluster_sync_all();  // every CTA's barriers exist before any cross-CTA signal
   tc_fence_after();
-  const uint32_t tmem_base = *tmem_slot;
-  const int entries = *entries_slot;
+  const uint32_t tmem_base = __shfl_sync(~0u, *tmem_slot, 0);
+  const int entries = __shfl_sync(~0u, *entries_slot, 0);
   const int64_t polls = prm.wait_polls;
   // the K blocks of this CTA
   const int kb0 = kPair ? 0 : static_cast<int>(static_cast<int64_t>(rank) * prm.k_blocks / csize);
@@ -280,21 +299,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int local = kPair ? t.width >> 1 : t.width;  // token rows this CTA loads
       const int j0 = kPair ? rank * local : 0;
       const int w_row = t.expert * prm.N + t.pb * C::PT + (kPair ? rank * 128 : 0);
-      int src[4] = {0, 0, 0, 0};
-      if (prm.row_token) {
-        // a row past the tile, or of no token, loads token 0: its column is
-        // dropped, or zeroed, by the epilogue
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int j = j0 + 4 * lane + i;
-          if (4 * lane < local && j < t.rows) src[i] = max(source_row(prm, t.row0 + j), 0);
-        }
-      }
       for (int kb = kb0; kb < kb1; ++kb) {
-        bool w = false;
-        if (lane == 0) w = wait_phase(EMPTY_BAR(stage), phase ^ 1u, polls, abort_flag);
-        w = __shfl_sync(~0u, w, 0);
-        if (!w) {
+        if (!__all_sync(~0u, wait_phase(EMPTY_BAR(stage), phase ^ 1u, polls, abort_flag))) {
           if (lane == 0) give_up();
           ok = false;
           break;
@@ -302,22 +308,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t sa = a_base + stage * C::A_BYTES, sb = b_base + stage * C::B_BYTES;
         // a pair's loads complete on the leader's barrier
         const uint32_t fb = kPair && rank ? map_to_cta(FULL_BAR(stage), 0) : FULL_BAR(stage);
-        if (lane == 0) {
+        if (elect_one()) {
           const uint32_t bytes = C::A_BYTES + local * BK;
           if (issues) mbar_arrive_expect_tx(FULL_BAR(stage), kPair ? 2 * bytes : bytes);
           if constexpr (kPair) tma_load_2d_pair(sa, &mapW, fb, kb * BK, w_row);
           else tma_load_2d(sa, &mapW, fb, kb * BK, w_row);
-        }
-        __syncwarp();
-        if (prm.row_token) {
-          if (4 * lane < local) {
-            if constexpr (kPair) tma_gather4_pair(sb + lane * 4 * BK, &mapX, fb, kb * BK, src);
-            else tma_gather4(sb + lane * 4 * BK, &mapX, fb, kb * BK, src);
+          if (!prm.row_token) {
+            // the tile's rows as boxes of falling powers of two
+            int j = 0;
+#pragma unroll
+            for (int i = 0; i < kBoxes; ++i) {
+              const int rows = 128 >> i;
+              if (j + rows <= local) {
+                if constexpr (kPair)
+                  tma_load_2d_pair(sb + j * BK, &mapX.m[i], fb, kb * BK, t.row0 + j0 + j);
+                else
+                  tma_load_2d(sb + j * BK, &mapX.m[i], fb, kb * BK, t.row0 + j0 + j);
+                j += rows;
+              }
+            }
           }
-        } else if (kBoxRows * lane < local) {
-          const int row = t.row0 + j0 + kBoxRows * lane;
-          if constexpr (kPair) tma_load_2d_pair(sb + lane * kBoxRows * BK, &mapX, fb, kb * BK, row);
-          else tma_load_2d(sb + lane * kBoxRows * BK, &mapX, fb, kb * BK, row);
         }
         if (++stage == STAGES) {
           stage = 0;
@@ -328,13 +338,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
+    // The issuer does not walk the table: a loop whose bounds come out of
+    // shared memory keeps the ring's stage, and with it every descriptor, out
+    // of the uniform registers that the MMA reads (measured 450-490 ns per
+    // 128-deep K step of a 256 x 256 pair tile, against 295 ns this way).  The
+    // scheduler hands it each tile's width bit by bit.
     if (issues) {
       int stage = 0;
       int acc = 0;
       bool ok = true;
-      while (ok && walk.next(t)) {
-        const uint32_t idesc = kF8 ? idesc_f8(C::PT, t.width) : idesc_i8(C::PT, t.width);
-        if (sched_sync(false)) break;  // the scheduler saw this accumulator free (or gave up)
+      while (ok) {
+        if (sched_sync(false)) break;  // no more tiles (or gave up); else the accumulator is free
+        uint32_t idesc = kF8 ? idesc_f8(C::PT, C::GRAIN) : idesc_i8(C::PT, C::GRAIN);
+#pragma unroll
+        for (int i = 0; i < C::WIDTH_BITS; ++i)
+          if (sched_sync(false)) idesc += static_cast<uint32_t>(C::GRAIN >> 3) << (17 + i);
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * C::QT);
         for (int kb = kb0; kb < kb1; ++kb) {
@@ -343,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           tc_fence_after();
-          if (lane == 0) {
+          if (elect_one()) {
             const uint32_t sa = a_base + stage * C::A_BYTES;
             const uint32_t sb = b_base + stage * C::B_BYTES;
 #pragma unroll
@@ -393,13 +411,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t phase = 0;
       int acc = 0;
       uint32_t acc_phase = 0;
-      bool ok = true;
+      bool ok = true, told = false;  // told: the issuer stopped inside a tile
       while (ok && walk.next(t)) {
         bool w = false;
         if (lane == 0) w = wait_phase(TEMPTY_BAR(acc), acc_phase ^ 1u, polls, abort_flag);
         w = __shfl_sync(~0u, w, 0);
-        if (!w && lane == 0) give_up();
-        if (sched_sync(!w)) break;
+        if (!w) {
+          if (lane == 0) give_up();
+          break;
+        }
+        sched_sync(false);
+#pragma unroll
+        for (int i = 0; i < C::WIDTH_BITS; ++i) sched_sync(((t.width / C::GRAIN - 1) >> i) & 1);
         for (int kb = kb0; kb < kb1; ++kb) {
           w = false;
           if (lane == 0) w = wait_phase(FULL_BAR(stage), phase, polls, abort_flag);
@@ -407,6 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!w && lane == 0) give_up();
           if (sched_sync(!w)) {
             ok = false;
+            told = true;
             break;
           }
           if (++stage == STAGES) {
@@ -416,6 +440,56 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
+      }
+      if (!told) sched_sync(true);  // the last tile is done
+    }
+  } else if (warp >= kGatherWarp) {
+    // ------------------------------------------------------------ token gather
+    // One thread per warp issues: a tile::gather4 takes uniform coordinates, and
+    // a warp whose lanes issue one each serialises them (measured 90 cycles
+    // apart: 2.3x the time of the whole tile).
+    if (prm.row_token) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      while (ok && walk.next(t)) {
+        const int local = kPair ? t.width >> 1 : t.width;
+        // every warp takes a quarter (a multiple of 4 rows): each has bytes in
+        // every stage, so none falls a phase behind the ring
+        const int mine = local / kGatherWarps;
+        const int g0 = (warp - kGatherWarp) * mine;
+        // a row past the tile, or of no token, loads token 0: its column is
+        // dropped, or zeroed, by the epilogue
+        const int j = (kPair ? rank * local : 0) + g0 + lane;
+        int found = 0;
+        if (lane < mine && j < t.rows) found = max(source_row(prm, t.row0 + j), 0);
+        int src[C::GATHER];
+#pragma unroll
+        for (int i = 0; i < C::GATHER; ++i) src[i] = __shfl_sync(~0u, found, i);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!__all_sync(~0u, wait_phase(EMPTY_BAR(stage), phase ^ 1u, polls, abort_flag))) {
+            if (lane == 0) give_up();
+            ok = false;
+            break;
+          }
+          const uint32_t fb = kPair && rank ? map_to_cta(FULL_BAR(stage), 0) : FULL_BAR(stage);
+          const uint32_t sb = b_base + stage * C::B_BYTES + g0 * BK;
+          if (elect_one()) {
+#pragma unroll
+            for (int i = 0; i < C::GATHER; i += 4) {
+              if (i < mine) {
+                const int rows[4] = {src[i], src[i + 1], src[i + 2], src[i + 3]};
+                if constexpr (kPair) tma_gather4_pair(sb + i * BK, &mapX.m[0], fb, kb * BK, rows);
+                else tma_gather4(sb + i * BK, &mapX.m[0], fb, kb * BK, rows);
+              }
+            }
+          }
+          __syncwarp();
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
       }
     }
   } else {
@@ -570,7 +644,7 @@ double active_experts(int64_t E, int64_t R) {
 }
 
 template <bool kPair, bool kF8>
-cudaError_t launch(const CUtensorMap& mw, const CUtensorMap& mx, const GroupedParams& prm,
+cudaError_t launch(const CUtensorMap& mw, const TokenMaps& mx, const GroupedParams& prm,
                    int64_t max_units, int sms, cudaStream_t st) {
   using C = Cfg<kPair>;
   auto kern = grouped_gemm_kernel<kPair, kF8>;
@@ -648,10 +722,15 @@ cudaError_t launch_gemm_grouped(const void* Xq, int64_t X, const void* Wq, const
     const double tiles = active_experts(E, R) * p.p_blocks;
     while (p.split < 4 && tiles * p.split < 0.75 * sms && 2 * p.split <= p.k_blocks) p.split *= 2;
   }
-  CUtensorMap mw, mx;
-  if (!make_code_map(&mw, Wq, E * N, K, 128) ||
-      !make_code_map(&mx, Xq, X, K, row_token ? 1 : kBoxRows))
-    return cudaErrorInvalidValue;
+  CUtensorMap mw;
+  TokenMaps mx;
+  bool ok = make_code_map(&mw, Wq, E * N, K, 128);
+  if (row_token) {
+    ok = ok && make_code_map(&mx.m[0], Xq, X, K, 1);
+  } else {
+    for (int i = 0; i < kBoxes; ++i) ok = ok && make_code_map(&mx.m[i], Xq, X, K, 128 >> i);
+  }
+  if (!ok) return cudaErrorInvalidValue;
   if (pair)
     return fp8 ? launch<true, true>(mw, mx, p, max_units, sms, st)
                : launch<true, false>(mw, mx, p, max_units, sms, st);
