@@ -62,7 +62,11 @@ struct Cfg {
   static constexpr int JOIN_SLOTS = kPair ? 0 : 3;     // partial sums of the other cluster ranks
   static constexpr int JOIN_BYTES = 128 * QT * 4;      // [token][128 weight rows]
   static constexpr int NUM_BARS = 2 * STAGES + 7;
-  static constexpr int TABLE = STAGES * STAGE_BYTES + JOIN_SLOTS * JOIN_BYTES;
+  static constexpr int OUT_BYTES = kPair ? 32 * 128 * 2 : 0;  // 32 tokens of bf16 outputs, twice
+  static constexpr int XS_BYTES = kPair ? QT * 4 : 0;         // a tile's token scales, twice
+  static constexpr int OUT = STAGES * STAGE_BYTES + JOIN_SLOTS * JOIN_BYTES;
+  static constexpr int XS = OUT + 2 * OUT_BYTES;
+  static constexpr int TABLE = XS + 2 * XS_BYTES;
   static constexpr int BARS = TABLE + kMaxExperts * 16;
   static constexpr int SMEM_BYTES = 1024 + BARS + 8 * NUM_BARS + 16;
   static constexpr int GATHER = Q_LOCAL / kGatherWarps;  // rows a gather warp loads at most
@@ -86,6 +90,7 @@ struct GroupedParams {
   void* out;
   int64_t ldo;
   int X, R, E, N, k_blocks, p_blocks, epi;
+  int vec_out;          // output rows 16-byte aligned
   int split;            // CTAs of a cluster that share a tile's K range (decode tiles)
   int64_t wait_polls;   // > 0: poll budget per wait; 0: ~2 s of SM clock cycles
   int* error_word;
@@ -180,6 +185,23 @@ __device__ __forceinline__ int source_row(const GroupedParams& p, int r) {
   const int s = __ldg(p.row_token + r);
   return s >= 0 && s < p.X ? s : -1;
 }
+
+// The four epilogue warps only; true where any of them gave up.
+__device__ __forceinline__ bool epilogue_sync(bool stop) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %1, 0;\n\t"
+      "bar.red.or.pred p, 2, 128, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(stop ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
+// In place of the scale of a row without a token: its outputs are zeros.
+constexpr uint32_t kNoToken = 0x80000000u;
 
 template <bool kF8>
 __device__ __forceinline__ float acc_value(uint32_t r) {
@@ -498,24 +520,119 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int p_local = quarter * 32 + lane;
     const bool raw = prm.epi == SQ_EPI_I32_RAW || prm.epi == SQ_EPI_F32_RAW;
     const bool relu = prm.epi == SQ_EPI_BF16_RELU;
+    float* xs_smem = reinterpret_cast<float*>(base_ptr + C::XS);
     int acc = 0;
     uint32_t acc_phase = 0, join_phase = 0;
     while (walk.next(t)) {
       const int n = t.pb * C::PT + (kPair ? rank * 128 : 0) + p_local;  // output column
       const bool n_in = n < prm.N;
       float ws = 0.0f;
-      if (!raw && n_in && (kPair || rank == 0))
+      if (!raw && n_in)
         ws = __ldg(prm.w_scale + static_cast<int64_t>(t.expert) * prm.N + n);
+      if constexpr (kPair) {
+        for (int j = static_cast<int>(threadIdx.x) - 64; j < t.rows; j += 128) {
+          const int s = source_row(prm, t.row0 + j);
+          float x = raw ? 1.0f : 0.0f;
+          if (s < 0) x = __uint_as_float(kNoToken);
+          else if (!raw) x = __ldg(prm.x_scale + s);
+          xs_smem[acc * C::QT + j] = x;
+        }
+      }
       bool w = false;
       if (lane == 0) w = wait_phase(TFULL_BAR(acc), acc_phase, polls, abort_flag);
       w = __shfl_sync(~0u, w, 0);
-      if (!w) {
-        if (lane == 0) give_up();
-        break;
+      if (!w && lane == 0) give_up();
+      if constexpr (kPair) {
+        // the tile's token scales are in shared memory, and no warp waits for
+        // one that gave up: past this point a tile has no way out but its end
+        if (epilogue_sync(!w)) break;
+      } else {
+        if (!w) break;
       }
       tc_fence_after();
       const uint32_t trow = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
                             static_cast<uint32_t>(acc * C::QT);
+      if constexpr (kPair) {
+        const float* xs_tile = xs_smem + acc * C::QT;
+#pragma unroll 1
+        for (int c = 0; c < t.rows; c += 32) {
+          uint32_t r[32];
+          __syncwarp();
+          tmem_ld_32x32b_x32(trow + static_cast<uint32_t>(c), r);
+          tmem_wait_ld();
+          if (c + 32 >= t.rows) {  // the accumulator is read: free it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if (rank) mbar_arrive_cluster(map_to_cta(TEMPTY_BAR(acc), 0));
+              else mbar_arrive(TEMPTY_BAR(acc));
+            }
+          }
+          const int64_t row = t.row0 + c;
+          if (raw) {
+            uint32_t* dst = static_cast<uint32_t*>(prm.out) + row * prm.ldo + n;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              if (c + j < t.rows && n_in)
+                *dst = __float_as_uint(xs_tile[c + j]) == kNoToken ? 0u : r[j];
+              dst += prm.ldo;
+            }
+            continue;
+          }
+          __nv_bfloat16 v[32];
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const float4 x4 = *reinterpret_cast<const float4*>(xs_tile + c + j);
+            const float xs[4] = {x4.x, x4.y, x4.z, x4.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float f = __fmul_rn(__fmul_rn(acc_value<kF8>(r[j + i]), xs[i]), ws);
+              if (__float_as_uint(xs[i]) == kNoToken) f = 0.0f;
+              if (relu) f = f > 0.0f ? f : 0.0f;  // -0 (a zero scale) becomes +0
+              v[j + i] = __float2bfloat16_rn(f);
+            }
+          }
+          if (!prm.vec_out) {
+            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(prm.out) + row * prm.ldo + n;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              if (c + j < t.rows && n_in) *dst = v[j];
+              dst += prm.ldo;
+            }
+            continue;
+          }
+          // lanes hold columns, rows are contiguous in memory: through shared
+          // memory, 256-byte pieces of the rows leave as 16-byte stores (the
+          // 2-byte stores above took 12.6 us of a 256 x 256 tile)
+          __nv_bfloat16* out_buf = reinterpret_cast<__nv_bfloat16*>(base_ptr + C::OUT) +
+                                   ((c >> 5) & 1) * (C::OUT_BYTES / 2);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) out_buf[j * 128 + p_local] = v[j];
+          epilogue_sync(false);  // two buffers: the next write here is two syncs away
+          const int et = static_cast<int>(threadIdx.x) - 64;
+          const int col = t.pb * C::PT + rank * 128 + (et & 15) * 8;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int j = (et >> 4) + 8 * k;
+            if (c + j < t.rows && col < prm.N) {
+              const uint4 w4 = *reinterpret_cast<const uint4*>(out_buf + j * 128 + (et & 15) * 8);
+              __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(prm.out) + (row + j) * prm.ldo + col;
+              if (col + 8 <= prm.N) {
+                *reinterpret_cast<uint4*>(dst) = w4;
+              } else {
+                const uint32_t u[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  if (col + i < prm.N)
+                    reinterpret_cast<uint16_t*>(dst)[i] = static_cast<uint16_t>(u[i >> 1] >> (16 * (i & 1)));
+              }
+            }
+          }
+        }
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+        continue;
+      }
       bool stop = false;
 #pragma unroll 1
       for (int c = 0; c < t.rows; c += 32) {
@@ -602,10 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (stop) break;
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        if (kPair && rank) mbar_arrive_cluster(map_to_cta(TEMPTY_BAR(acc), 0));
-        else mbar_arrive(TEMPTY_BAR(acc));
-      }
+      if (lane == 0) mbar_arrive(TEMPTY_BAR(acc));
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
     }
@@ -712,6 +826,7 @@ cudaError_t launch_gemm_grouped(const void* Xq, int64_t X, const void* Wq, const
   const int pt = pair ? 256 : 128, qt = pair ? 256 : 32;
   p.p_blocks = static_cast<int>((N + pt - 1) / pt);
   p.epi = epi;
+  p.vec_out = (reinterpret_cast<uintptr_t>(out) & 15u) == 0 && ldo % 8 == 0;
   p.split = 1;
   p.wait_polls = wait_polls;
   p.error_word = error_word;
