@@ -711,8 +711,8 @@ sq_status sq_moe_route(const void* logits, sq_dtype dtype, int64_t T, int64_t E,
  *   epi      SQ_EPI_BF16, SQ_EPI_BF16_RELU or SQ_EPI_I32_RAW
  *   out      device [R, N], row stride ldo; rows outside [offsets[0],
  *            offsets[E]) are left as they were
- *   path_hint  0 = automatic, 1 = prefill tiles (CTA pairs), 2 = decode tiles
- *            (weight blocks of 128 rows, K split over a small cluster)
+ *   path_hint  0 = automatic, 1 = prefill tiles (CTA pairs, up to 256 tokens),
+ *            2 = decode tiles (weight blocks of 128 rows, up to 32 tokens)
  * E <= SQ_MOE_MAX_EXPERTS.
  * Errors: those of sq_w8a8_gemm_dequant.
  */
@@ -724,8 +724,7 @@ sq_status sq_w8a8_gemm_grouped(const int8_t* Xq, int64_t X, const int8_t* Wq,
 
 /*
  * sq_fp8_gemm_grouped -- the same on e4m3 codes with an fp32 accumulator (as
- * sq_fp8_gemm_dequant; the raw epilogue is SQ_EPI_F32_RAW).  K ranges split
- * over a cluster are added in a fixed order.
+ * sq_fp8_gemm_dequant; the raw epilogue is SQ_EPI_F32_RAW).
  */
 sq_status sq_fp8_gemm_grouped(const uint8_t* Xq8, int64_t X, const uint8_t* Wq8,
                               const float* x_scale, const float* w_scale,

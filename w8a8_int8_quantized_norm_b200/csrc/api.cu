@@ -653,7 +653,9 @@ sq_status gemm_grouped(const void* Xq, int64_t X, const void* Wq, const float* x
   if (epi != raw && (!x_scale || !w_scale)) return SQ_ERR_INVALID_ARG;
   if (K > SQ_MAX_K) return SQ_ERR_OVERFLOW_RISK;
   // tensor-map coordinates and row numbers are 32-bit
-  if (X > 0x7fffffff || R > 0x7fffffff || N > 0x7fffffff / E) return SQ_ERR_UNSUPPORTED;
+  // (a tile may reach 256 rows past either's end)
+  const int64_t top = 0x7fffffff - 512;
+  if (X > top || R > top || N > top / E) return SQ_ERR_UNSUPPORTED;
   // so are tile numbers: at most one tile per 16 rows (and expert) and 128 columns
   if ((R / 16 + E + 1) * (N / 128 + 1) > 0x3fffffff) return SQ_ERR_UNSUPPORTED;
   const uintptr_t esz = epi == raw ? 4 : 2;

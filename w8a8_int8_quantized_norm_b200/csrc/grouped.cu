@@ -11,10 +11,8 @@
 // costs MMA time and token loads for little more than its own rows.
 //   pair tiles   (prefill) 256 weight rows x up to 256 tokens on a CTA pair
 //                (cta_group::2), two accumulators in tensor memory;
-//   decode tiles 128 weight rows x up to 32 tokens per CTA, the weight stream's
-//                K range split over a cluster of up to 4 CTAs when there are too
-//                few tiles to fill the SMs; the partial sums meet through
-//                distributed shared memory, added in rank order by rank 0.
+//   decode tiles 128 weight rows x up to 32 tokens per CTA, eight stages in
+//                flight (ten measured the same).
 // Every CTA first turns the offsets into a table of the non-empty experts and
 // their tiles; persistent CTAs then walk the flattened tiles, a weight block's
 // token tiles next to each other, so a weight byte comes from HBM once.
@@ -26,7 +24,6 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
-#include <math.h>
 #include <stdint.h>
 
 #include <atomic>
@@ -51,7 +48,6 @@ template <bool kPair>
 struct Cfg {
   static constexpr int QT = kPair ? 256 : 32;          // tokens of a tile at most
   static constexpr int GRAIN = kPair ? 32 : 16;        // tile widths are multiples of this
-  static constexpr int WIDTH_BITS = kPair ? 3 : 1;     // of width / GRAIN - 1
   static constexpr int PT = kPair ? 256 : 128;         // weight rows of a tile
   static constexpr int Q_LOCAL = kPair ? QT / 2 : QT;  // token rows a CTA loads at most
   static constexpr int A_BYTES = 128 * BK;
@@ -59,12 +55,10 @@ struct Cfg {
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int STAGES = kPair ? 6 : 8;
   static constexpr int TMEM_COLS = kPair ? 512 : 64;   // two accumulators
-  static constexpr int JOIN_SLOTS = kPair ? 0 : 3;     // partial sums of the other cluster ranks
-  static constexpr int JOIN_BYTES = 128 * QT * 4;      // [token][128 weight rows]
-  static constexpr int NUM_BARS = 2 * STAGES + 7;
+  static constexpr int NUM_BARS = 2 * STAGES + 5;
   static constexpr int OUT_BYTES = kPair ? 32 * 128 * 2 : 0;  // 32 tokens of bf16 outputs, twice
   static constexpr int XS_BYTES = kPair ? QT * 4 : 0;         // a tile's token scales, twice
-  static constexpr int OUT = STAGES * STAGE_BYTES + JOIN_SLOTS * JOIN_BYTES;
+  static constexpr int OUT = STAGES * STAGE_BYTES;
   static constexpr int XS = OUT + 2 * OUT_BYTES;
   static constexpr int TABLE = XS + 2 * XS_BYTES;
   static constexpr int BARS = TABLE + kMaxExperts * 16;
@@ -73,7 +67,6 @@ struct Cfg {
   static_assert(GATHER <= 32 && GATHER % 4 == 0, "a lane finds one row's token");
   static_assert((kPair ? GRAIN / 2 : GRAIN) % (4 * kGatherWarps) == 0, "a gather4 per warp");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
-  static_assert(QT == GRAIN << WIDTH_BITS, "a tile's width in WIDTH_BITS bits");
   static_assert(STAGE_BYTES % 1024 == 0, "swizzle atoms need 1024-byte aligned stages");
 };
 
@@ -91,7 +84,6 @@ struct GroupedParams {
   int64_t ldo;
   int X, R, E, N, k_blocks, p_blocks, epi;
   int vec_out;          // output rows 16-byte aligned
-  int split;            // CTAs of a cluster that share a tile's K range (decode tiles)
   int64_t wait_polls;   // > 0: poll budget per wait; 0: ~2 s of SM clock cycles
   int* error_word;
 };
@@ -179,13 +171,6 @@ struct Walk {
   }
 };
 
-// The row of Xq a row of the grouped matrix reads, or -1.
-__device__ __forceinline__ int source_row(const GroupedParams& p, int r) {
-  if (!p.row_token) return r;
-  const int s = __ldg(p.row_token + r);
-  return s >= 0 && s < p.X ? s : -1;
-}
-
 // The four epilogue warps only; true where any of them gave up.
 __device__ __forceinline__ bool epilogue_sync(bool stop) {
   uint32_t r;
@@ -209,18 +194,6 @@ __device__ __forceinline__ float acc_value(uint32_t r) {
   else return __int2float_rn(static_cast<int>(r));
 }
 
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 template <bool kPair, bool kF8>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_gemm_kernel(const __grid_constant__ CUtensorMap mapW,
@@ -233,7 +206,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* base_ptr = smem_raw + (base - raw_u32);
   const uint32_t a_base = base;
   const uint32_t b_base = base + STAGES * C::A_BYTES;
-  const uint32_t join_base = base + STAGES * C::STAGE_BYTES;
   Entry* table = reinterpret_cast<Entry*>(base_ptr + C::TABLE);
   const uint32_t bar_base = base + C::BARS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base_ptr + C::BARS + 8 * C::NUM_BARS);
@@ -244,16 +216,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #define TFULL_BAR(a) (bar_base + 8u * static_cast<uint32_t>(2 * STAGES + (a)))
 #define TEMPTY_BAR(a) (bar_base + 8u * static_cast<uint32_t>(2 * STAGES + 2 + (a)))
 #define DRAIN_BAR (bar_base + 8u * static_cast<uint32_t>(2 * STAGES + 4))
-#define JOIN_FULL_BAR (bar_base + 8u * static_cast<uint32_t>(2 * STAGES + 5))
-#define JOIN_EMPTY_BAR (bar_base + 8u * static_cast<uint32_t>(2 * STAGES + 6))
 
   const int warp = __shfl_sync(~0u, static_cast<int>(threadIdx.x) >> 5, 0);
   const int lane = threadIdx.x & 31;
-  const int csize = kPair ? 2 : prm.split;  // CTAs of the cluster
-  const int rank = csize > 1 ? __shfl_sync(~0u, static_cast<int>(cluster_ctarank()), 0) : 0;
-  const bool issues = !kPair || rank == 0;  // this CTA's warp 1 issues MMAs
-  const int id = static_cast<int>(blockIdx.x) / csize;
-  const int clusters = static_cast<int>(gridDim.x) / csize;
+  const int rank = kPair ? __shfl_sync(~0u, static_cast<int>(cluster_ctarank()), 0) : 0;
+  const bool issues = rank == 0;  // this CTA's warp 1 issues MMAs
+  const int id = static_cast<int>(blockIdx.x) / (kPair ? 2 : 1);
+  const int workers = static_cast<int>(gridDim.x) / (kPair ? 2 : 1);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -265,8 +234,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(TEMPTY_BAR(a), kPair ? 8 : 4);
     }
     mbar_init(DRAIN_BAR, 1);
-    mbar_init(JOIN_FULL_BAR, csize > 1 ? 4 * (csize - 1) : 1);  // every warp of the other ranks
-    mbar_init(JOIN_EMPTY_BAR, 4);                               // rank 0's epilogue warps
     *abort_flag = 0;
     mbar_fence_init();
   }
@@ -293,23 +260,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (csize > 1) cluster_sync_all();  // every CTA's barriers exist before any cross-CTA signal
+  if (kPair) cluster_sync_all();  // every CTA's barriers exist before any cross-CTA signal
   tc_fence_after();
   const uint32_t tmem_base = __shfl_sync(~0u, *tmem_slot, 0);
   const int entries = __shfl_sync(~0u, *entries_slot, 0);
   const int64_t polls = prm.wait_polls;
-  // the K blocks of this CTA
-  const int kb0 = kPair ? 0 : static_cast<int>(static_cast<int64_t>(rank) * prm.k_blocks / csize);
-  const int kb1 = kPair ? prm.k_blocks
-                        : static_cast<int>(static_cast<int64_t>(rank + 1) * prm.k_blocks / csize);
-  Walk<kPair> walk(prm, table, entries, id, clusters);
+  Walk<kPair> walk(prm, table, entries, id, workers);
   Tile t;
 
-  // a wait ran out: stop every CTA of the cluster
+  // a wait ran out: stop this CTA and its partner
   auto give_up = [&]() {
     fail(prm.error_word, abort_flag);
-    for (int c = 0; c < csize; ++c)
-      if (c != rank) st_cluster_u32(map_to_cta(smem_u32(const_cast<int*>(abort_flag)), c), 1u);
+    if (kPair) st_cluster_u32(map_to_cta(smem_u32(const_cast<int*>(abort_flag)), rank ^ 1), 1u);
   };
 
   if (warp == 0) {
@@ -321,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int local = kPair ? t.width >> 1 : t.width;  // token rows this CTA loads
       const int j0 = kPair ? rank * local : 0;
       const int w_row = t.expert * prm.N + t.pb * C::PT + (kPair ? rank * 128 : 0);
-      for (int kb = kb0; kb < kb1; ++kb) {
+      for (int kb = 0; kb < prm.k_blocks; ++kb) {
         if (!__all_sync(~0u, wait_phase(EMPTY_BAR(stage), phase ^ 1u, polls, abort_flag))) {
           if (lane == 0) give_up();
           ok = false;
@@ -360,24 +322,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    // The issuer does not walk the table: a loop whose bounds come out of
-    // shared memory keeps the ring's stage, and with it every descriptor, out
-    // of the uniform registers that the MMA reads (measured 450-490 ns per
-    // 128-deep K step of a 256 x 256 pair tile, against 295 ns this way).  The
-    // scheduler hands it each tile's width bit by bit.
     if (issues) {
       int stage = 0;
       int acc = 0;
       bool ok = true;
-      while (ok) {
-        if (sched_sync(false)) break;  // no more tiles (or gave up); else the accumulator is free
-        uint32_t idesc = kF8 ? idesc_f8(C::PT, C::GRAIN) : idesc_i8(C::PT, C::GRAIN);
-#pragma unroll
-        for (int i = 0; i < C::WIDTH_BITS; ++i)
-          if (sched_sync(false)) idesc += static_cast<uint32_t>(C::GRAIN >> 3) << (17 + i);
+      while (ok && walk.next(t)) {
+        const uint32_t idesc = kF8 ? idesc_f8(C::PT, t.width) : idesc_i8(C::PT, t.width);
+        if (sched_sync(false)) break;  // the scheduler saw the accumulator free (or gave up)
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * C::QT);
-        for (int kb = kb0; kb < kb1; ++kb) {
+        for (int kb = 0; kb < prm.k_blocks; ++kb) {
           if (sched_sync(false)) {  // the scheduler saw this stage land (or gave up)
             ok = false;
             break;
@@ -390,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int kk = 0; kk < BK / UMMA_K; ++kk) {
               const uint64_t da = smem_desc_k_sw128(sa + kk * UMMA_K);
               const uint64_t db = smem_desc_k_sw128(sb + kk * UMMA_K);
-              const uint32_t add = (kb > kb0 || kk > 0) ? 1u : 0u;
+              const uint32_t add = (kb > 0 || kk > 0) ? 1u : 0u;
               if constexpr (kPair && kF8) mma_f8_pair(d_tmem, da, db, idesc, add);
               else if constexpr (kPair) mma_i8_pair(d_tmem, da, db, idesc, add);
               else if constexpr (kF8) mma_f8(d_tmem, da, db, idesc, add);
@@ -407,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (++stage == STAGES) stage = 0;
         }
         if (!ok) break;
-        if (lane == 0) {
+        if (elect_one()) {  // the same lane every time: a commit covers its thread's MMAs
           if constexpr (kPair) {
             mma_commit_pair(TFULL_BAR(acc));
             mma_commit_pair(map_to_cta(TFULL_BAR(acc), 1));
@@ -418,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         acc ^= 1;
       }
-      if (lane == 0) {
+      if (elect_one()) {
         // every MMA issued by this thread completes before tensor memory is freed
         if constexpr (kPair) mma_commit_pair(DRAIN_BAR);
         else mma_commit(DRAIN_BAR);
@@ -433,26 +387,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t phase = 0;
       int acc = 0;
       uint32_t acc_phase = 0;
-      bool ok = true, told = false;  // told: the issuer stopped inside a tile
+      bool ok = true;
       while (ok && walk.next(t)) {
         bool w = false;
         if (lane == 0) w = wait_phase(TEMPTY_BAR(acc), acc_phase ^ 1u, polls, abort_flag);
         w = __shfl_sync(~0u, w, 0);
-        if (!w) {
-          if (lane == 0) give_up();
-          break;
-        }
-        sched_sync(false);
-#pragma unroll
-        for (int i = 0; i < C::WIDTH_BITS; ++i) sched_sync(((t.width / C::GRAIN - 1) >> i) & 1);
-        for (int kb = kb0; kb < kb1; ++kb) {
+        if (!w && lane == 0) give_up();
+        if (sched_sync(!w)) break;
+        for (int kb = 0; kb < prm.k_blocks; ++kb) {
           w = false;
           if (lane == 0) w = wait_phase(FULL_BAR(stage), phase, polls, abort_flag);
           w = __shfl_sync(~0u, w, 0);
           if (!w && lane == 0) give_up();
           if (sched_sync(!w)) {
             ok = false;
-            told = true;
             break;
           }
           if (++stage == STAGES) {
@@ -463,32 +411,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
       }
-      if (!told) sched_sync(true);  // the last tile is done
     }
   } else if (warp >= kGatherWarp) {
     // ------------------------------------------------------------ token gather
-    // One thread per warp issues: a tile::gather4 takes uniform coordinates, and
-    // a warp whose lanes issue one each serialises them (measured 90 cycles
+    // An elected lane issues: a tile::gather4 takes uniform coordinates, and a
+    // warp whose lanes issue one each serialises them (measured 90 cycles
     // apart: 2.3x the time of the whole tile).
     if (prm.row_token) {
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      while (ok && walk.next(t)) {
-        const int local = kPair ? t.width >> 1 : t.width;
-        // every warp takes a quarter (a multiple of 4 rows): each has bytes in
-        // every stage, so none falls a phase behind the ring
+      // The token of this lane's row, a tile ahead: the load's latency passes
+      // while the tile before is copied.  Every warp takes a quarter of a tile
+      // (a multiple of 4 rows): each has bytes in every stage, so none falls a
+      // phase behind the ring.
+      auto find = [&](const Tile& a) {
+        const int local = kPair ? a.width >> 1 : a.width;
         const int mine = local / kGatherWarps;
+        const int j = (kPair ? rank * local : 0) + (warp - kGatherWarp) * mine + lane;
+        return lane < mine && j < a.rows ? __ldg(prm.row_token + a.row0 + j) : 0;
+      };
+      bool live = walk.next(t);
+      int found = live ? find(t) : 0;
+      while (ok && live) {
+        Tile ahead;
+        const bool more = walk.next(ahead);
+        const int found_ahead = more ? find(ahead) : 0;
+        const int mine = (kPair ? t.width >> 1 : t.width) / kGatherWarps;
         const int g0 = (warp - kGatherWarp) * mine;
         // a row past the tile, or of no token, loads token 0: its column is
         // dropped, or zeroed, by the epilogue
-        const int j = (kPair ? rank * local : 0) + g0 + lane;
-        int found = 0;
-        if (lane < mine && j < t.rows) found = max(source_row(prm, t.row0 + j), 0);
+        if (found < 0 || found >= prm.X) found = 0;
         int src[C::GATHER];
 #pragma unroll
         for (int i = 0; i < C::GATHER; ++i) src[i] = __shfl_sync(~0u, found, i);
-        for (int kb = kb0; kb < kb1; ++kb) {
+        for (int kb = 0; kb < prm.k_blocks; ++kb) {
           if (!__all_sync(~0u, wait_phase(EMPTY_BAR(stage), phase ^ 1u, polls, abort_flag))) {
             if (lane == 0) give_up();
             ok = false;
@@ -512,6 +469,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             phase ^= 1u;
           }
         }
+        t = ahead;
+        live = more;
+        found = found_ahead;
       }
     }
   } else {
@@ -520,23 +480,61 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int p_local = quarter * 32 + lane;
     const bool raw = prm.epi == SQ_EPI_I32_RAW || prm.epi == SQ_EPI_F32_RAW;
     const bool relu = prm.epi == SQ_EPI_BF16_RELU;
+    const int et = static_cast<int>(threadIdx.x) - 64;
     float* xs_smem = reinterpret_cast<float*>(base_ptr + C::XS);
     int acc = 0;
-    uint32_t acc_phase = 0, join_phase = 0;
-    while (walk.next(t)) {
-      const int n = t.pb * C::PT + (kPair ? rank * 128 : 0) + p_local;  // output column
-      const bool n_in = n < prm.N;
-      float ws = 0.0f;
-      if (!raw && n_in)
-        ws = __ldg(prm.w_scale + static_cast<int64_t>(t.expert) * prm.N + n);
-      if constexpr (kPair) {
-        for (int j = static_cast<int>(threadIdx.x) - 64; j < t.rows; j += 128) {
-          const int s = source_row(prm, t.row0 + j);
-          float x = raw ? 1.0f : 0.0f;
-          if (s < 0) x = __uint_as_float(kNoToken);
-          else if (!raw) x = __ldg(prm.x_scale + s);
-          xs_smem[acc * C::QT + j] = x;
+    uint32_t acc_phase = 0;
+    // What a tile needs from global memory, loaded ahead of it: its rows' tokens
+    // two tiles before, their scales and the columns' scale one tile before, so
+    // that neither latency falls between two tiles (few K blocks: it was most
+    // of the tile's time).  Pair tiles: thread et holds tokens et and et + 128;
+    // decode tiles: lane l token l.
+    constexpr int NT = kPair ? 2 : 1;
+    struct Ahead {
+      Tile t;
+      bool live;
+      int src[NT];
+      float xs[NT], ws;
+    };
+    auto load_rows = [&](Ahead& a) {
+      a.live = walk.next(a.t);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const int j = kPair ? et + 128 * i : lane;
+        a.src[i] = -1;
+        if (a.live && j < a.t.rows) {
+          a.src[i] = a.t.row0 + j;
+          if (prm.row_token) a.src[i] = __ldg(prm.row_token + a.src[i]);
         }
+      }
+    };
+    auto column = [&](const Tile& a) { return a.pb * C::PT + (kPair ? rank * 128 : 0) + p_local; };
+    auto load_scales = [&](Ahead& a) {
+      if (!a.live) return;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        a.xs[i] = __uint_as_float(kNoToken);
+        if (a.src[i] >= 0 && a.src[i] < prm.X)
+          a.xs[i] = raw ? 1.0f : __ldg(prm.x_scale + a.src[i]);
+      }
+      const int n = column(a.t);
+      a.ws = !raw && n < prm.N
+                 ? __ldg(prm.w_scale + static_cast<int64_t>(a.t.expert) * prm.N + n) : 0.0f;
+    };
+    Ahead cur, nxt, far;
+    load_rows(cur);
+    load_rows(nxt);
+    load_scales(cur);
+    for (; cur.live; cur = nxt, nxt = far) {
+      load_rows(far);
+      load_scales(nxt);
+      t = cur.t;
+      const float ws = cur.ws;
+      const int n = column(t);  // this thread's output column
+      const bool n_in = n < prm.N;
+      if constexpr (kPair) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) xs_smem[acc * C::QT + et + 128 * i] = cur.xs[i];
       }
       bool w = false;
       if (lane == 0) w = wait_phase(TFULL_BAR(acc), acc_phase, polls, abort_flag);
@@ -609,7 +607,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) out_buf[j * 128 + p_local] = v[j];
           epilogue_sync(false);  // two buffers: the next write here is two syncs away
-          const int et = static_cast<int>(threadIdx.x) - 64;
           const int col = t.pb * C::PT + rank * 128 + (et & 15) * 8;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -633,90 +630,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (acc == 0) acc_phase ^= 1u;
         continue;
       }
-      bool stop = false;
-#pragma unroll 1
-      for (int c = 0; c < t.rows; c += 32) {
+      {  // QT = 32: one chunk
         uint32_t r[32];
         __syncwarp();
-        tmem_ld_32x32b_x32(trow + static_cast<uint32_t>(c), r);
-        // lane j holds what column c + j needs
-        const int row = t.row0 + c + lane;
-        int s = -1;
-        if (c + lane < t.rows) s = source_row(prm, row);
-        const float xs_l = !raw && s >= 0 ? __ldg(prm.x_scale + s) : 0.0f;
-        const uint32_t zero = __ballot_sync(~0u, s < 0);
+        tmem_ld_32x32b_x32(trow, r);
+        const uint32_t zero = __ballot_sync(~0u, __float_as_uint(cur.xs[0]) == kNoToken);
         tmem_wait_ld();
-        if constexpr (!kPair) {
-          if (csize > 1) {  // QT = 32: one chunk per tile
-            if (rank > 0) {
-              // partial sums to rank 0's slot, once it has read the last ones
-              if (lane == 0) w = wait_phase(JOIN_EMPTY_BAR, join_phase ^ 1u, polls, abort_flag);
-              w = __shfl_sync(~0u, w, 0);
-              if (!w) {
-                if (lane == 0) give_up();
-                stop = true;
-                break;
-              }
-              const uint32_t dst = map_to_cta(
-                  join_base + (rank - 1) * C::JOIN_BYTES + p_local * 4, 0);
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (j < t.rows) st_cluster_u32(dst + j * 512, r[j]);
-              asm volatile("fence.acq_rel.cluster;" ::: "memory");
-              __syncwarp();
-              if (lane == 0) mbar_arrive_cluster(map_to_cta(JOIN_FULL_BAR, 0));
-            } else {
-              if (lane == 0) w = wait_phase(JOIN_FULL_BAR, join_phase, polls, abort_flag);
-              w = __shfl_sync(~0u, w, 0);
-              if (!w) {
-                if (lane == 0) give_up();
-                stop = true;
-                break;
-              }
-              mbar_try_wait_cluster(JOIN_FULL_BAR, join_phase);  // complete: acquires the stores
-              for (int o = 0; o < csize - 1; ++o) {
-                const uint32_t* src = reinterpret_cast<const uint32_t*>(
-                    base_ptr + (join_base - base) + o * C::JOIN_BYTES) + p_local;
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  if (j < t.rows) {
-                    const uint32_t v = src[j * 128];
-                    if constexpr (kF8)
-                      r[j] = __float_as_uint(__fadd_rn(__uint_as_float(r[j]), __uint_as_float(v)));
-                    else
-                      r[j] += v;
-                  }
-              }
-              __syncwarp();
-              if (lane == 0)
-                for (int o = 1; o < csize; ++o) mbar_arrive_cluster(map_to_cta(JOIN_EMPTY_BAR, o));
-            }
-            join_phase ^= 1u;
-            if (rank > 0) continue;
-          }
-        }
         if (raw) {
-          uint32_t* dst = static_cast<uint32_t*>(prm.out) + static_cast<int64_t>(t.row0 + c) * prm.ldo + n;
+          uint32_t* dst = static_cast<uint32_t*>(prm.out) + static_cast<int64_t>(t.row0) * prm.ldo + n;
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
-            if (c + j < t.rows && n_in) *dst = (zero >> j) & 1u ? 0u : r[j];
+            if (j < t.rows && n_in) *dst = (zero >> j) & 1u ? 0u : r[j];
             dst += prm.ldo;
           }
         } else {
           __nv_bfloat16* dst =
-              static_cast<__nv_bfloat16*>(prm.out) + static_cast<int64_t>(t.row0 + c) * prm.ldo + n;
+              static_cast<__nv_bfloat16*>(prm.out) + static_cast<int64_t>(t.row0) * prm.ldo + n;
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
-            const float xs = __shfl_sync(~0u, xs_l, j);
+            const float xs = __shfl_sync(~0u, cur.xs[0], j);
             float v = __fmul_rn(__fmul_rn(acc_value<kF8>(r[j]), xs), ws);
             if ((zero >> j) & 1u) v = 0.0f;
             if (relu) v = v > 0.0f ? v : 0.0f;  // -0 (a zero scale) becomes +0
-            if (c + j < t.rows && n_in) *dst = __float2bfloat16_rn(v);
+            if (j < t.rows && n_in) *dst = __float2bfloat16_rn(v);
             dst += prm.ldo;
           }
         }
       }
-      if (stop) break;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(TEMPTY_BAR(acc));
@@ -725,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   __syncthreads();
-  if (csize > 1) cluster_sync_all();  // no MMA, load signal or remote store is pending
+  if (kPair) cluster_sync_all();  // no MMA, load signal or remote store is pending
   if (*abort_flag) {
     // after an abort some loads may still be in flight, and the barriers that
     // would tell may never complete: about 20 ms, thousands of times a load's
@@ -735,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   __syncthreads();
-  if (csize > 1) cluster_sync_all();
+  if (kPair) cluster_sync_all();
   if (warp == 1) {
     tc_fence_after();
     if constexpr (kPair) tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
@@ -746,15 +686,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #undef TFULL_BAR
 #undef TEMPTY_BAR
 #undef DRAIN_BAR
-#undef JOIN_FULL_BAR
-#undef JOIN_EMPTY_BAR
-}
-
-// Experts that get at least one of R rows, at even popularity.
-double active_experts(int64_t E, int64_t R) {
-  if (E <= 1) return 1.0;
-  return static_cast<double>(E) *
-         -expm1(static_cast<double>(R) * log1p(-1.0 / static_cast<double>(E)));
 }
 
 template <bool kPair, bool kF8>
@@ -764,7 +695,7 @@ cudaError_t launch(const CUtensorMap& mw, const TokenMaps& mx, const GroupedPara
   auto kern = grouped_gemm_kernel<kPair, kF8>;
   cudaError_t e = launch_cache().ensure_smem(reinterpret_cast<const void*>(kern), C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  const int csize = kPair ? 2 : prm.split;
+  constexpr int csize = kPair ? 2 : 1;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -777,18 +708,18 @@ cudaError_t launch(const CUtensorMap& mw, const TokenMaps& mx, const GroupedPara
   cfg.dynamicSmemBytes = C::SMEM_BYTES;
   cfg.stream = st;
   cfg.attrs = attr;
-  cfg.numAttrs = csize > 1 ? 2 : 1;
+  cfg.numAttrs = kPair ? 2 : 1;
   int64_t clusters = sms / csize;
-  if (csize > 1) {
-    // as many clusters as the device holds at once, asked once per device and size
-    static std::atomic<int> held[64][5];
+  if (kPair) {
+    // as many pairs as the device holds at once, asked once per device
+    static std::atomic<int> held[64];
     const int dev = LaunchCache::device();
-    int n = dev >= 0 && dev < 64 ? held[dev][csize].load() : 0;
+    int n = dev >= 0 && dev < 64 ? held[dev].load() : 0;
     if (n == 0) {
       cfg.gridDim = dim3(static_cast<unsigned>(clusters * csize));
       if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0)
         n = static_cast<int>(clusters);
-      if (dev >= 0 && dev < 64) held[dev][csize].store(n);
+      if (dev >= 0 && dev < 64) held[dev].store(n);
     }
     if (n < clusters) clusters = n;
   }
@@ -807,9 +738,9 @@ cudaError_t launch_gemm_grouped(const void* Xq, int64_t X, const void* Wq, const
                                 int num_sms, int64_t wait_polls, int* error_word, bool fp8,
                                 cudaStream_t st) {
   const int sms = num_sms > 0 ? num_sms : 148;
-  // decode tiles while an expert has few rows: they keep twice as many weight
-  // blocks in flight; past 32 rows an expert's weights would be read again for
-  // every 32
+  // decode tiles while an expert has few rows: they keep more weight blocks in
+  // flight and need no cluster; past 32 rows an expert's weights would be read
+  // again for every 32
   const bool pair = path_hint == 1 || (path_hint == 0 && R > 24 * E);
   GroupedParams p{};
   p.x_scale = x_scale;
@@ -827,16 +758,10 @@ cudaError_t launch_gemm_grouped(const void* Xq, int64_t X, const void* Wq, const
   p.p_blocks = static_cast<int>((N + pt - 1) / pt);
   p.epi = epi;
   p.vec_out = (reinterpret_cast<uintptr_t>(out) & 15u) == 0 && ldo % 8 == 0;
-  p.split = 1;
   p.wait_polls = wait_polls;
   p.error_word = error_word;
   const int64_t max_units = ((R + qt - 1) / qt + (E < R ? E : R)) * p.p_blocks;
   if (max_units > 0x3fffffff) return cudaErrorInvalidValue;
-  if (!pair) {
-    // enough clusters to fill the SMs, by the tiles to be expected
-    const double tiles = active_experts(E, R) * p.p_blocks;
-    while (p.split < 4 && tiles * p.split < 0.75 * sms && 2 * p.split <= p.k_blocks) p.split *= 2;
-  }
   CUtensorMap mw;
   TokenMaps mx;
   bool ok = make_code_map(&mw, Wq, E * N, K, 128);
