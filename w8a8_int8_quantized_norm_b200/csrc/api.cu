@@ -715,7 +715,10 @@ sq_status block_norm(const sq_block_norm_args* args, bool fp8, void* stream) {
   if (overlap(a.Xq, a.M * a.K, a.x, nx) || overlap(a.Xq, a.M * a.K, a.residual, nr) ||
       overlap(a.Xq, a.M * a.K, a.h_out, nh))
     return SQ_ERR_INVALID_ARG;
-  return from_cuda(launch_block_norm(a, fp8, as_stream(stream)));
+  int* err = device_error_word();
+  if (!err) return SQ_ERR_CUDA;
+  return from_cuda(
+      launch_block_norm(a, fp8, sms_cached(), g_wait_polls.load(), err, as_stream(stream)));
 }
 
 }  // namespace

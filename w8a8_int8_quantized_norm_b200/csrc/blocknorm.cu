@@ -28,8 +28,16 @@ struct BlockNormParams {
   sq_block_norm_args a;
   int K;
   int fp8;
-  int stages;  // reductions before the codes' (for the shared-memory slots)
 };
+
+// Rows pass through once: they leave L1 to the parameter vectors.
+__device__ __forceinline__ uint4 load_stream(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
 
 // 8 consecutive values as loaded: 16 bytes of bf16 or 32 bytes of fp32.
 template <typename T>
@@ -38,21 +46,23 @@ template <>
 struct Raw8<__nv_bfloat16> {
   uint4 w;
   __device__ __forceinline__ void load(const void* p, int64_t i) {
-    w = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i);
+    w = load_stream(static_cast<const __nv_bfloat16*>(p) + i);
   }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
+  // 16 bytes a lane: all banks once
+  __device__ __forceinline__ void load_shared(const uint8_t* buf, int c) {
+    w = *reinterpret_cast<const uint4*>(buf + c * 16);
+  }
+  __device__ __forceinline__ void get(float2 (&v)[4]) const {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] = __uint_as_float(u[j] << 16);
-      v[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
-    }
+    for (int j = 0; j < 4; ++j)
+      v[j] = make_float2(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xffff0000u));
   }
-  static __device__ __forceinline__ void store(void* p, int64_t i, const float* v) {
+  static __device__ __forceinline__ void store(void* p, int64_t i, const float2 (&v)[4]) {
     uint32_t u[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[j].x, v[j].y);
       u[j] = *reinterpret_cast<const uint32_t*>(&h);
     }
     *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + i) = make_uint4(u[0], u[1], u[2], u[3]);
@@ -60,162 +70,237 @@ struct Raw8<__nv_bfloat16> {
 };
 template <>
 struct Raw8<float> {
-  float4 lo, hi;
+  uint4 lo, hi;
   __device__ __forceinline__ void load(const void* p, int64_t i) {
-    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-    lo = q[0];
-    hi = q[1];
+    const float* q = static_cast<const float*>(p) + i;
+    lo = load_stream(q);
+    hi = load_stream(q + 4);
   }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-    v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
-    v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
+  __device__ __forceinline__ void load_shared(const uint8_t* buf, int c) {
+    lo = *reinterpret_cast<const uint4*>(buf + c * 32);
+    hi = *reinterpret_cast<const uint4*>(buf + c * 32 + 16);
   }
-  static __device__ __forceinline__ void store(void* p, int64_t i, const float* v) {
+  __device__ __forceinline__ void get(float2 (&v)[4]) const {
+    const uint32_t u[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      v[j] = make_float2(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
+  }
+  static __device__ __forceinline__ void store(void* p, int64_t i, const float2 (&v)[4]) {
     float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
-    q[0] = make_float4(v[0], v[1], v[2], v[3]);
-    q[1] = make_float4(v[4], v[5], v[6], v[7]);
+    q[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    q[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
   }
 };
 
-__device__ __forceinline__ void load_vec8(const float* p, int i, float (&v)[8]) {
-  const float4* q = reinterpret_cast<const float4*>(p + i);
-  const float4 a = __ldg(q), b = __ldg(q + 1);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+// 8 parameters of chunk c: from global memory as they are, or from the shared
+// copy, whose two halves lie apart (16 bytes a lane: all banks once).
+struct GlobalVec {
+  const float* p;
+  __device__ __forceinline__ void get(int c, float2 (&g)[4]) const {
+    const float4* q = reinterpret_cast<const float4*>(p + c * 8);
+    const float4 a = __ldg(q), b = __ldg(q + 1);
+    g[0] = make_float2(a.x, a.y);
+    g[1] = make_float2(a.z, a.w);
+    g[2] = make_float2(b.x, b.y);
+    g[3] = make_float2(b.z, b.w);
+  }
+};
+struct SharedVec {
+  uint32_t addr;  // 0: none
+  int half;       // bytes between the halves
+  __device__ __forceinline__ explicit operator bool() const { return addr != 0; }
+  __device__ __forceinline__ void get(int c, float2 (&g)[4]) const {
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(g[0].x), "=f"(g[0].y), "=f"(g[1].x), "=f"(g[1].y)
+                 : "r"(addr + c * 16));
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(g[2].x), "=f"(g[2].y), "=f"(g[3].x), "=f"(g[3].y)
+                 : "r"(addr + half + c * 16));
+  }
+};
+
+template <typename V>
+__device__ __forceinline__ void mul8(float2 (&v)[4], const V& p, int c) {
+  float2 g[4];
+  p.get(c, g);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = __fmul2_rn(v[j], g[j]);
+}
+template <typename V>
+__device__ __forceinline__ void add8(float2 (&v)[4], const V& p, int c) {
+  float2 b[4];
+  p.get(c, b);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = __fadd2_rn(v[j], b[j]);
+}
+__device__ __forceinline__ void fma8(float2 (&v)[4], float w, const float2 (&t)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = __ffma2_rn(make_float2(w, w), t[j], v[j]);
+}
+__device__ __forceinline__ void scale8(float2 (&v)[4], float w) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = __fmul2_rn(v[j], make_float2(w, w));
 }
 
-// Sum over the CTA; `slot` is a 32-entry row of shared memory no other
+// The warps that share a row: a whole CTA, or one of its groups.
+struct Team {
+  int thread, threads, warps, bar;  // bar: named barrier of a group, 0 for the CTA's
+  __device__ __forceinline__ void sync() const {
+    asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(threads) : "memory");
+  }
+};
+
+// Sum over the team; `slot` is a 32-entry row of shared memory no other
 // reduction of the same row uses.  Every thread gets the same bits.
-__device__ __forceinline__ float cta_sum(float v, float* slot, int warps) {
+__device__ __forceinline__ float team_sum(float v, float* slot, const Team& tm) {
 #pragma unroll
   for (int s = 16; s > 0; s >>= 1) v += __shfl_xor_sync(~0u, v, s);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = tm.thread >> 5, warps = tm.warps, lane = threadIdx.x & 31;
   if (lane == 0) slot[warp] = v;
-  __syncthreads();
+  tm.sync();
   float t = lane < warps ? slot[lane] : 0.0f;
 #pragma unroll
   for (int s = 16; s > 0; s >>= 1) t += __shfl_xor_sync(~0u, t, s);
   return t;
 }
 
-// Max of |.| bit patterns: NaN's lie above infinity's, so a NaN survives.
-__device__ __forceinline__ uint32_t cta_max(uint32_t v, float* slot, int warps) {
-  v = __reduce_max_sync(~0u, v);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (lane == 0) slot[warp] = __uint_as_float(v);
-  __syncthreads();
-  return __reduce_max_sync(~0u, lane < warps ? __float_as_uint(slot[lane]) : 0u);
+__device__ __forceinline__ float max_nan(float a, float b) {  // a NaN survives
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
 
-// INT8 codes of 8 values: rne(fl32(v / step)).  v * fl32(1 / step) is within
-// 2^-22 relative of that quotient, under 4e-5 for |code| <= 127; only a
-// product that near a half-integer can round another way and is divided.
-__device__ __forceinline__ uint2 codes_i8(const float* v, float step, float inv) {
-  float t[8], frac = 0.0f;
-  int q[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    t[j] = __fmul_rn(v[j], inv);
-    const float r = rintf(t[j]);
-    frac = fmaxf(frac, fabsf(t[j] - r));
-    q[j] = static_cast<int>(r);
-  }
-  if (!(frac < 0.5f - 4e-5f && step >= FLT_MIN && step <= FLT_MAX)) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) q[j] = quant_code(v[j], step);
-  }
-  uint32_t w[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-    w[h] = (q[4 * h] & 0xff) | ((q[4 * h + 1] & 0xff) << 8) | ((q[4 * h + 2] & 0xff) << 16) |
-           (static_cast<uint32_t>(q[4 * h + 3]) << 24);
-  return make_uint2(w[0], w[1]);
+// Max over the team of values >= 0 (or NaN, whose bits order above infinity's).
+__device__ __forceinline__ float team_max(float v, float* slot, const Team& tm) {
+  const uint32_t u = __reduce_max_sync(~0u, __float_as_uint(v) & 0x7fffffffu);
+  const int warp = tm.thread >> 5, warps = tm.warps, lane = threadIdx.x & 31;
+  if (lane == 0) slot[warp] = __uint_as_float(u);
+  tm.sync();
+  return __uint_as_float(
+      __reduce_max_sync(~0u, lane < warps ? __float_as_uint(slot[lane]) : 0u));
 }
 
-__device__ __forceinline__ uint2 codes_f8(const float* v, float inv) {
-  uint32_t w[2];
+// INT8 codes of 8 values: rne(fl32(v / step)).  Adding 1.5 2^23 leaves the
+// integer in the low byte.  v fl32(inv (1 - 2^-21)) and v fl32(inv (1 + 2^-21)),
+// inv = fl32(1 / step), lie on either side of v / step and of its fp32
+// rounding (each off by at most 2^-23 relative); when both round to the same
+// integer that is the code, else the quotient itself is taken.
+__device__ __forceinline__ uint2 codes_i8(const float2 (&v)[4], float step, float inv) {
+  const float lo = __fmul_rn(inv, 1.0f - 0x1p-21f), hi = __fmul_rn(inv, 1.0f + 0x1p-21f);
+  const float2 magic = make_float2(12582912.0f, 12582912.0f);
+  uint32_t q[8], differ = 0;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(
-        make_float2(__fmul_rn(v[4 * h], inv), __fmul_rn(v[4 * h + 1], inv)), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(
-        make_float2(__fmul_rn(v[4 * h + 2], inv), __fmul_rn(v[4 * h + 3], inv)), __NV_SATFINITE,
-        __NV_E4M3);
-    w[h] = lo | (hi << 16);
+  for (int j = 0; j < 4; ++j) {
+    const float2 a = __ffma2_rn(v[j], make_float2(lo, lo), magic);
+    const float2 b = __ffma2_rn(v[j], make_float2(hi, hi), magic);
+    q[2 * j] = __float_as_uint(a.x);
+    q[2 * j + 1] = __float_as_uint(a.y);
+    differ |= (q[2 * j] ^ __float_as_uint(b.x)) | (q[2 * j + 1] ^ __float_as_uint(b.y));
   }
-  return make_uint2(w[0], w[1]);
+  // outside this range (zero, subnormal, huge, not finite) inv is no reciprocal
+  if (differ != 0 || !(step >= FLT_MIN && step <= 0x1p125f)) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      q[2 * j] = static_cast<uint32_t>(quant_code(v[j].x, step));
+      q[2 * j + 1] = static_cast<uint32_t>(quant_code(v[j].y, step));
+    }
+  }
+  return make_uint2(
+      __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410),
+      __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410));
 }
 
-// v (this thread's chunks) -> norm(v), in place.  Two reductions for
-// LayerNorm, one for RMSNorm, none without a norm.
+__device__ __forceinline__ uint2 codes_f8(const float2 (&v)[4], float inv) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    w[j] = __nv_cvt_float2_to_fp8x2(__fmul2_rn(v[j], make_float2(inv, inv)), __NV_SATFINITE,
+                                    __NV_E4M3);
+  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+}
+
+// v (this thread's chunks) -> its norm before gamma and beta, in place.  Two
+// reductions for LayerNorm, one for RMSNorm, none without a norm.
 template <int CH>
-__device__ __forceinline__ void apply_norm(float (&v)[CH][8], int K, int norm, const float* gamma,
-                                           const float* beta, float eps, float (*slots)[32],
-                                           int warps) {
-  const int chunks = K >> 3;
-  float mu = 0.0f, r = 1.0f;
+__device__ __forceinline__ void normalise(float2 (&v)[CH][4], int K, int norm, float eps,
+                                          float (*slots)[32], const Team& tm) {
+  if (norm == SQ_NORM_NONE) return;
+  const float inv_k = __frcp_rn(static_cast<float>(K));
+  float2 s[2];
   if (norm == SQ_NORM_LAYER) {
-    float s = 0.0f;
+    s[0] = s[1] = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < CH; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s += v[i][j];
-    mu = cta_sum(s, slots[0], warps) / static_cast<float>(K);
+      for (int j = 0; j < 4; ++j) s[j & 1] = __fadd2_rn(s[j & 1], v[i][j]);
+    const float mu =
+        team_sum((s[0].x + s[0].y) + (s[1].x + s[1].y), slots[0], tm) * inv_k;
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+      if (tm.thread + i * tm.threads < (K >> 3)) {  // the rest of v stays zero
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[i][j] = __fadd2_rn(v[i][j], make_float2(-mu, -mu));
+      }
   }
-  if (norm != SQ_NORM_NONE) {
-    float s[2] = {0.0f, 0.0f};
+  s[0] = s[1] = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int c = static_cast<int>(threadIdx.x) + i * static_cast<int>(blockDim.x);
-      if (c < chunks) {
+  for (int i = 0; i < CH; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          v[i][j] -= mu;
-          s[j & 1] = fmaf(v[i][j], v[i][j], s[j & 1]);
-        }
+    for (int j = 0; j < 4; ++j) s[j & 1] = __ffma2_rn(v[i][j], v[i][j], s[j & 1]);
+  const float var =
+      team_sum((s[0].x + s[0].y) + (s[1].x + s[1].y), slots[1], tm) * inv_k;
+  const float r = rsqrtf(var + eps);  // within 2 units in the last place
+#pragma unroll
+  for (int i = 0; i < CH; ++i) scale8(v[i], r);
+}
+
+// The codes of y and their scale; one reduction.
+template <int CH>
+__device__ __forceinline__ void store_codes(const float2 (&v)[CH][4], const BlockNormParams& p,
+                                            int64_t m, float* slot, const Team& tm) {
+  float am[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < CH; ++i)
+    if (tm.thread + i * tm.threads < (p.K >> 3)) {  // a row of NaN leaves them past its end too
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        am[0] = max_nan(am[0], fabsf(v[i][j].x));
+        am[1] = max_nan(am[1], fabsf(v[i][j].y));
       }
     }
-    const float var = cta_sum(s[0] + s[1], slots[1], warps) / static_cast<float>(K);
-    r = 1.0f / sqrtf(var + eps);
-  }
+  const float amax = team_max(max_nan(am[0], am[1]), slot, tm);
+  float step = __fdiv_rn(amax, p.fp8 ? 448.0f : 127.0f);
+  if (p.fp8 && step < FLT_MIN) step = 0.0f;
+  const float inv = step != 0.0f ? __fdiv_rn(1.0f, step) : 0.0f;
+  if (tm.thread == 0) p.a.x_scale[m] = step;
+  uint8_t* q = static_cast<uint8_t*>(p.a.Xq) + m * p.K;
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
-    const int c = static_cast<int>(threadIdx.x) + i * static_cast<int>(blockDim.x);
-    if (c < chunks) {
-      if (norm != SQ_NORM_NONE) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] *= r;
-      }
-      if (gamma) {
-        float g[8];
-        load_vec8(gamma, c * 8, g);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] *= g[j];
-      }
-      if (beta && norm == SQ_NORM_LAYER) {
-        float b[8];
-        load_vec8(beta, c * 8, b);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] += b[j];
-      }
-    }
+    const int c = tm.thread + i * tm.threads;
+    if (c < (p.K >> 3))
+      *reinterpret_cast<uint2*>(q + c * 8) =
+          p.fp8 ? codes_f8(v[i], inv) : codes_i8(v[i], step, inv);
   }
 }
 
+// One row per CTA, straight from global memory: few rows, and rows whose
+// parameters and buffers do not fit the pipeline below.
 template <typename T, int CH, int kMaxThreads>
 __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const BlockNormParams p) {
   __shared__ float slots[5][32];
   const sq_block_norm_args& a = p.a;
   const int chunks = p.K >> 3;
-  const int warps = static_cast<int>(blockDim.x) >> 5;
+  const Team tm{static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x),
+                static_cast<int>(blockDim.x) >> 5, 0};
   const int64_t m = blockIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  float v[CH][8];
+  float2 v[CH][4];
 #pragma unroll
   for (int i = 0; i < CH; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+    for (int j = 0; j < 4; ++j) v[i][j] = make_float2(0.0f, 0.0f);
   if (a.token_row) {
     for (int k = 0; k < a.top_k; ++k) {
       const int64_t row = a.token_row[m * a.top_k + k];
@@ -223,21 +308,20 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const BlockNorm
       const float w = a.weights[m * a.top_k + k];
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
-        const int c = static_cast<int>(threadIdx.x) + i * static_cast<int>(blockDim.x);
+        const int c = tm.thread + i * tm.threads;
         if (c < chunks) {
           Raw8<T> raw;
           raw.load(a.x, row * a.ldx + c * 8);
-          float t[8];
+          float2 t[4];
           raw.get(t);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[i][j] = fmaf(w, t[j], v[i][j]);
+          fma8(v[i], w, t);
         }
       }
     }
   } else {
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int c = static_cast<int>(threadIdx.x) + i * static_cast<int>(blockDim.x);
+      const int c = tm.thread + i * tm.threads;
       if (c < chunks) {
         Raw8<T> raw;
         raw.load(a.x, m * a.ldx + c * 8);
@@ -245,78 +329,331 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const BlockNorm
       }
     }
   }
-  apply_norm<CH>(v, p.K, a.post_norm, a.post_gamma, a.post_beta, a.post_eps, slots, warps);
+  // the residual is on its way through the first norm's reductions
+  Raw8<T> res[CH];
+  if (a.residual) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = tm.thread + i * tm.threads;
+      if (c < chunks) res[i].load(a.residual, m * a.ld_res + c * 8);
+    }
+  }
   const float tg = a.token_gate ? a.token_gate[m] : 1.0f;
+  normalise<CH>(v, p.K, a.post_norm, a.post_eps, slots, tm);
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
-    const int c = static_cast<int>(threadIdx.x) + i * static_cast<int>(blockDim.x);
+    const int c = tm.thread + i * tm.threads;
     if (c < chunks) {
-      if (a.gate) {
-        float g[8];
-        load_vec8(a.gate, c * 8, g);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] *= g[j];
-      }
-      if (a.token_gate) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] *= tg;
-      }
+      if (a.post_gamma) mul8(v[i], GlobalVec{a.post_gamma}, c);
+      if (a.post_beta && a.post_norm == SQ_NORM_LAYER) add8(v[i], GlobalVec{a.post_beta}, c);
+      if (a.gate) mul8(v[i], GlobalVec{a.gate}, c);
+      if (a.token_gate) scale8(v[i], tg);
       if (a.residual) {
-        Raw8<T> raw;
-        raw.load(a.residual, m * a.ld_res + c * 8);
-        float t[8];
-        raw.get(t);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = fmaf(a.residual_scale, t[j], v[i][j]);
+        float2 t[4];
+        res[i].get(t);
+        fma8(v[i], a.residual_scale, t);
       }
       if (a.h_out) Raw8<T>::store(a.h_out, m * a.ld_h + c * 8, v[i]);
     }
   }
   if (!a.Xq) return;
-  apply_norm<CH>(v, p.K, a.pre_norm, a.pre_gamma, a.pre_beta, a.pre_eps, slots + 2, warps);
-  uint32_t am = 0;
+  normalise<CH>(v, p.K, a.pre_norm, a.pre_eps, slots + 2, tm);
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
-    const int c = static_cast<int>(threadIdx.x) + i * static_cast<int>(blockDim.x);
+    const int c = tm.thread + i * tm.threads;
     if (c < chunks) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) am = max(am, __float_as_uint(v[i][j]) & 0x7fffffffu);
+      if (a.pre_gamma) mul8(v[i], GlobalVec{a.pre_gamma}, c);
+      if (a.pre_beta && a.pre_norm == SQ_NORM_LAYER) add8(v[i], GlobalVec{a.pre_beta}, c);
     }
   }
-  const float amax = __uint_as_float(cta_max(am, slots[4], warps));
-  float step = __fdiv_rn(amax, p.fp8 ? 448.0f : 127.0f);
-  if (p.fp8 && step < FLT_MIN) step = 0.0f;
-  const float inv = step != 0.0f ? __fdiv_rn(1.0f, step) : 0.0f;
-  if (threadIdx.x == 0) a.x_scale[m] = step;
-  uint8_t* q = static_cast<uint8_t*>(a.Xq) + m * p.K;
-#pragma unroll
-  for (int i = 0; i < CH; ++i) {
-    const int c = static_cast<int>(threadIdx.x) + i * static_cast<int>(blockDim.x);
-    if (c < chunks)
-      *reinterpret_cast<uint2*>(q + c * 8) =
-          p.fp8 ? codes_f8(v[i], inv) : codes_i8(v[i], step, inv);
-  }
+  store_codes<CH>(v, p, m, slots[4], tm);
+}
+
+// ---------------------------------------------------------------------------
+// Many rows: one persistent CTA per SM, its warps in groups of a row each.  A
+// group's inputs arrive by cp.async.bulk into its own shared-memory buffers:
+// the next row's x is fetched as soon as this row's is in registers, the next
+// residual after this one, so copies are in flight through the reductions and
+// stores; with plain loads the kernel waited for them (long-scoreboard stalls
+// 8.6 of 15 warps, a third of HBM).  The parameter vectors (post_gamma * gate,
+// post_beta * gate, pre_gamma, pre_beta) are put into shared memory once per
+// CTA: read per row through L1 they were more bytes than the row itself.
+// ---------------------------------------------------------------------------
+constexpr int kPipeCH = 4;
+constexpr int kMaxGroups = 8;
+constexpr int kPipeMaxK = 8192;  // 256 threads a row at most
+constexpr int kPipeMaxSum = 4;   // expert rows a token sums, at most
+
+struct PipeShape {
+  int groups, threads;         // threads of a group
+  int x_rows;                  // buffers of x rows per group
+  int vecs;                    // parameter vectors in shared memory
+  int vec_at[4];               // slot of A, B, C, D, or -1
+  int row_bytes, smem;
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// mbarrier.try_wait that may suspend the thread for up to `ns` nanoseconds.
+__device__ __forceinline__ bool mbar_try_wait_for(uint32_t bar, uint32_t parity, uint32_t ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(ns)
+      : "memory");
+  return ok != 0;
 }
 
 template <typename T>
-cudaError_t launch_block_norm_t(const BlockNormParams& p, cudaStream_t st) {
+__device__ __forceinline__ void shared8(const uint8_t* buf, int c, float2 (&v)[4]) {
+  Raw8<T> raw;
+  raw.load_shared(buf, c);
+  raw.get(v);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(1024, 1)
+    block_norm_pipe_kernel(const BlockNormParams p, const PipeShape sh, int* error_word,
+                           int64_t wait_polls) {
+  constexpr int CH = kPipeCH;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float slots[kMaxGroups][5][32];
+  __shared__ uint64_t bars[kMaxGroups][2];
+  __shared__ float sum_w[kMaxGroups][2][kPipeMaxSum];  // weights of the row being fetched, by parity
+  __shared__ int sum_ok[kMaxGroups][2];                // which of its rows exist, a bit each
+  __shared__ int abort_flag;
+  const sq_block_norm_args& a = p.a;
+  const int chunks = p.K >> 3;
+  const int g = static_cast<int>(threadIdx.x) / sh.threads;
+  const Team tm{static_cast<int>(threadIdx.x) - g * sh.threads, sh.threads, sh.threads >> 5, 1 + g};
+  float* params = reinterpret_cast<float*>(smem);
+  uint8_t* xbuf = smem + static_cast<size_t>(sh.vecs) * p.K * 4 +
+                  static_cast<size_t>(g) * (sh.x_rows + (a.residual ? 1 : 0)) * sh.row_bytes;
+  uint8_t* rbuf = xbuf + sh.x_rows * sh.row_bytes;
+  const uint32_t xbar = smem_u32(&bars[g][0]), rbar = smem_u32(&bars[g][1]);
+  const int64_t step_rows = static_cast<int64_t>(gridDim.x) * sh.groups;
+  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * sh.groups + g;
+
+  if (threadIdx.x == 0) abort_flag = 0;
+  if (tm.thread == 0) {
+    mbar_init(xbar, 1);
+    mbar_init(rbar, 1);
+    mbar_fence_init();
+  }
+  if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  // The group's first warp fetches.  Lane j < top_k has the j-th expert row and
+  // weight of the next row to fetch, read a row ahead (peek).
+  const int lane = static_cast<int>(threadIdx.x) & 31;
+  const bool fetcher = tm.thread < 32;
+  int next_row = -1;
+  float next_w = 0.0f;
+  auto peek = [&](int64_t m) {
+    next_row = -1;
+    if (a.token_row && lane < a.top_k && m < a.M) {
+      next_row = a.token_row[m * a.top_k + lane];
+      next_w = a.weights[m * a.top_k + lane];
+    }
+  };
+  auto fetch_x = [&](int64_t m, int parity) {
+    if (!a.token_row) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(xbar, sh.row_bytes);
+        bulk_load(smem_u32(xbuf), static_cast<const T*>(a.x) + m * a.ldx, sh.row_bytes, xbar);
+      }
+      return;
+    }
+    const bool mine = next_row >= 0 && next_row < a.R;
+    const uint32_t ok = __ballot_sync(~0u, mine);
+    if (lane < a.top_k) sum_w[g][parity][lane] = next_w;
+    if (lane == 0) sum_ok[g][parity] = static_cast<int>(ok);
+    __syncwarp();
+    if (lane == 0) mbar_arrive_expect_tx(xbar, __popc(ok) * sh.row_bytes);
+    __syncwarp();
+    if (mine)
+      bulk_load(smem_u32(xbuf) + lane * sh.row_bytes,
+                static_cast<const T*>(a.x) + static_cast<int64_t>(next_row) * a.ldx, sh.row_bytes,
+                xbar);
+  };
+  auto fetch_res = [&](int64_t m) {
+    mbar_arrive_expect_tx(rbar, sh.row_bytes);
+    bulk_load(smem_u32(rbuf), static_cast<const T*>(a.residual) + m * a.ld_res, sh.row_bytes, rbar);
+  };
+  if (fetcher && m0 < a.M) {
+    peek(m0);
+    fetch_x(m0, 0);
+    if (a.residual && lane == 0) fetch_res(m0);
+    peek(m0 + step_rows);
+  }
+  // the parameters, the halves of every 8 apart
+  for (int i = threadIdx.x; i < p.K; i += blockDim.x) {
+    const int at = ((i & 4) ? p.K / 2 : 0) + (i >> 3) * 4 + (i & 3);
+    const float g1 = a.gate ? a.gate[i] : 1.0f;
+    if (sh.vec_at[0] >= 0)
+      params[sh.vec_at[0] * p.K + at] = (a.post_gamma ? a.post_gamma[i] : 1.0f) * g1;
+    if (sh.vec_at[1] >= 0) params[sh.vec_at[1] * p.K + at] = a.post_beta[i] * g1;
+    if (sh.vec_at[2] >= 0) params[sh.vec_at[2] * p.K + at] = a.pre_gamma[i];
+    if (sh.vec_at[3] >= 0) params[sh.vec_at[3] * p.K + at] = a.pre_beta[i];
+  }
+  SharedVec vec[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    vec[i] = SharedVec{sh.vec_at[i] >= 0 ? smem_u32(params + sh.vec_at[i] * p.K) : 0u, p.K * 2};
+  __syncthreads();
+
+  uint32_t phase = 0;
+  // The first probe sleeps up to 20 us in hardware: a group that spins takes
+  // issue slots from the ones at work.  A wait that runs out is recorded; the
+  // rows still go through (their barriers must be met), without waiting any more.
+  auto wait = [&](uint32_t bar) {
+    if (wait_polls <= 0 && mbar_try_wait_for(bar, phase, 20000u)) return;
+    if (!wait_phase(bar, phase, wait_polls, &abort_flag)) {
+      record_device_error(error_word, SQ_ERR_PIPELINE_TIMEOUT);
+      *const_cast<volatile int*>(&abort_flag) = 1;
+    }
+  };
+  for (int64_t m = m0; m < a.M; m += step_rows, phase ^= 1u) {
+    const bool more = m + step_rows < a.M;
+    float2 v[CH][4];
+    const float tg = a.token_gate ? __ldg(a.token_gate + m) : 1.0f;
+    wait(xbar);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[i][j] = make_float2(0.0f, 0.0f);
+      const int c = tm.thread + i * tm.threads;
+      if (c < chunks) {
+        if (!a.token_row) {
+          shared8<T>(xbuf, c, v[i]);
+        } else {
+          const int ok = sum_ok[g][phase];
+          for (int k = 0; k < a.top_k; ++k) {
+            if ((ok >> k) & 1) {
+              const float w = sum_w[g][phase][k];
+              float2 t[4];
+              shared8<T>(xbuf + k * sh.row_bytes, c, t);
+              fma8(v[i], w, t);
+            }
+          }
+        }
+      }
+    }
+    if (a.post_norm == SQ_NORM_NONE) tm.sync();  // the row is in registers (else: by the sum)
+    normalise<CH>(v, p.K, a.post_norm, a.post_eps, slots[g], tm);
+    if (fetcher && more) {
+      fetch_x(m + step_rows, phase ^ 1u);
+      peek(m + 2 * step_rows);
+    }
+    if (a.residual) wait(rbar);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = tm.thread + i * tm.threads;
+      if (c < chunks) {
+        if (vec[0]) mul8(v[i], vec[0], c);
+        if (vec[1]) add8(v[i], vec[1], c);
+        if (a.token_gate) scale8(v[i], tg);
+        if (a.residual) {
+          float2 t[4];
+          shared8<T>(rbuf, c, t);
+          fma8(v[i], a.residual_scale, t);
+        }
+        if (a.h_out) Raw8<T>::store(a.h_out, m * a.ld_h + c * 8, v[i]);
+      }
+    }
+    if (a.Xq) {
+      normalise<CH>(v, p.K, a.pre_norm, a.pre_eps, slots[g] + 2, tm);
+      // (a sum's barrier, or the maximum's below, follows the residual's reads)
+      const bool early = a.pre_norm != SQ_NORM_NONE;
+      if (a.residual && early && tm.thread == 0 && more) fetch_res(m + step_rows);
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const int c = tm.thread + i * tm.threads;
+        if (c < chunks) {
+          if (vec[2]) mul8(v[i], vec[2], c);
+          if (vec[3]) add8(v[i], vec[3], c);
+        }
+      }
+      store_codes<CH>(v, p, m, slots[g][4], tm);
+      if (a.residual && !early && tm.thread == 0 && more) fetch_res(m + step_rows);
+    } else {
+      tm.sync();
+      if (a.residual && tm.thread == 0 && more) fetch_res(m + step_rows);
+    }
+  }
+  if (*const_cast<volatile int*>(&abort_flag)) {
+    // about 20 ms: every copy in flight lands before the shared memory goes
+    const long long t0 = clock64();
+    while (clock64() - t0 < 40000000LL) {
+    }
+  }
+}
+
+// Groups of the pipeline for these arguments, or false if it does not pay:
+// fewer than two groups fit (their copies would not overlap a row's
+// reductions), or there are too few rows to fill it twice (measured on 148
+// SMs, 4096 channels: see the launch below).
+bool pipe_shape(const sq_block_norm_args& a, int sms, PipeShape& sh) {
+  const int K = static_cast<int>(a.K), es = a.dtype == SQ_BF16 ? 2 : 4;
+  if (K > kPipeMaxK || a.top_k > kPipeMaxSum) return false;
+  sh.vecs = 0;
+  const bool has[4] = {a.post_gamma || a.gate, a.post_beta && a.post_norm == SQ_NORM_LAYER,
+                       a.Xq && a.pre_gamma,
+                       a.Xq && a.pre_beta && a.pre_norm == SQ_NORM_LAYER};
+  for (int i = 0; i < 4; ++i) sh.vec_at[i] = has[i] ? sh.vecs++ : -1;
+  sh.threads = ((K / 8 + kPipeCH - 1) / kPipeCH + 31) / 32 * 32;
+  sh.x_rows = a.top_k > 0 ? a.top_k : 1;
+  sh.row_bytes = K * es;
+  const int group = (sh.x_rows + (a.residual ? 1 : 0)) * sh.row_bytes;
+  const int room = 220 * 1024 - sh.vecs * K * 4;
+  int n = room / group;
+  if (n > 1024 / sh.threads) n = 1024 / sh.threads;
+  if (n > kMaxGroups) n = kMaxGroups;
+  if (n < 2 || a.M < static_cast<int64_t>(2) * n * sms) return false;
+  sh.groups = n;
+  sh.smem = sh.vecs * K * 4 + n * group;
+  return true;
+}
+
+template <typename T>
+cudaError_t launch_block_norm_t(const BlockNormParams& p, int sms, int64_t wait_polls,
+                                int* error_word, cudaStream_t st) {
   const int chunks = p.K >> 3;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.a.M));
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  PipeShape sh;
+  if (pipe_shape(p.a, sms, sh)) {
+    auto kern = block_norm_pipe_kernel<T>;
+    cudaError_t e = launch_cache().ensure_smem(reinterpret_cast<const void*>(kern), sh.smem);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(static_cast<unsigned>(sms));
+    cfg.blockDim = dim3(static_cast<unsigned>(sh.groups * sh.threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(sh.smem);
+    return cudaLaunchKernelEx(&cfg, kern, p, sh, error_word, wait_polls);
+  }
+  cfg.gridDim = dim3(static_cast<unsigned>(p.a.M));
   auto threads = [&](int ch) { return static_cast<unsigned>(((chunks + ch - 1) / ch + 31) / 32 * 32); };
   if (chunks <= 1024) {
     cfg.blockDim = dim3(threads(1));
     return cudaLaunchKernelEx(&cfg, block_norm_kernel<T, 1, 1024>, p);
   }
   if (chunks <= 2048) {
-    cfg.blockDim = dim3(threads(4));
-    return cudaLaunchKernelEx(&cfg, block_norm_kernel<T, 4, 512>, p);
+    cfg.blockDim = dim3(threads(2));
+    return cudaLaunchKernelEx(&cfg, block_norm_kernel<T, 2, 1024>, p);
   }
   cfg.blockDim = dim3(threads(8));
   return cudaLaunchKernelEx(&cfg, block_norm_kernel<T, 8, 512>, p);
@@ -324,14 +661,17 @@ cudaError_t launch_block_norm_t(const BlockNormParams& p, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_block_norm(const sq_block_norm_args& a, bool fp8, cudaStream_t st) {
+cudaError_t launch_block_norm(const sq_block_norm_args& a, bool fp8, int num_sms,
+                              int64_t wait_polls, int* error_word, cudaStream_t st) {
   if (a.M == 0) return cudaSuccess;
+  const int sms = num_sms > 0 ? num_sms : 148;
   BlockNormParams p{};
   p.a = a;
   p.K = static_cast<int>(a.K);
   p.fp8 = fp8 ? 1 : 0;
-  return a.dtype == SQ_BF16 ? launch_block_norm_t<__nv_bfloat16>(p, st)
-                            : launch_block_norm_t<float>(p, st);
+  return a.dtype == SQ_BF16
+             ? launch_block_norm_t<__nv_bfloat16>(p, sms, wait_polls, error_word, st)
+             : launch_block_norm_t<float>(p, sms, wait_polls, error_word, st);
 }
 
 }  // namespace sq

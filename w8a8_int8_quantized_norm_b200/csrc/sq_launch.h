@@ -150,7 +150,8 @@ cudaError_t launch_gemm_grouped(const void* Xq, int64_t X, const void* Wq, const
                                 cudaStream_t st);
 
 // blocknorm.cu (the end of one block and the start of the next)
-cudaError_t launch_block_norm(const sq_block_norm_args& a, bool fp8, cudaStream_t st);
+cudaError_t launch_block_norm(const sq_block_norm_args& a, bool fp8, int num_sms,
+                              int64_t wait_polls, int* error_word, cudaStream_t st);
 
 // gemm.cu
 struct GemmPlan {

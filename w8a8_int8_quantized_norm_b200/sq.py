@@ -662,6 +662,15 @@ class MoeRoute(NamedTuple):
     token_row: torch.Tensor  # [T, top_k] int32, the row of each token's j-th expert, -1: none
 
 
+# The current stream's handle and the current device, without building the
+# Python objects around them: a single-token call costs about as much host time
+# as these do (3.2 us of torch.cuda.current_stream() against 0.1 us).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_NO_SCOPE = contextlib.nullcontext()
+
+
 def _scope(device: torch.device, stream):
     """The context of a call on tensors of ``device``: that device current, and
     what the call allocates taken from the memory of the stream it runs on."""
@@ -669,25 +678,18 @@ def _scope(device: torch.device, stream):
         if stream.device != device:
             raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, device))
         return torch.cuda.stream(stream)
-    if torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+    return _NO_SCOPE if _raw_device() == device.index else torch.cuda.device(device)
 
 
 def _dense(t: Optional[torch.Tensor], shape, dtype, device, name: str):
-    """A contiguous tensor of exactly this shape, type and device (or None)."""
-    if t is not None and (t.dtype != dtype or t.shape != shape or t.device != device
-                          or not t.is_contiguous()):
+    """Address of a contiguous tensor of exactly this shape, type and device
+    (None of None)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor of shape %s on %s"
                          % (name, dtype, list(shape), device))
-    return t
-
-
-def _out(t: Optional[torch.Tensor], shape, dtype, device, name: str):
-    """The caller's output tensor, or a new one."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    return _dense(t, shape, dtype, device, name)
+    return t.data_ptr()
 
 
 def moe_route_workspace_size(T: int, E: int, top_k: int) -> int:
@@ -707,55 +709,73 @@ def moe_route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias=Non
         raise ValueError("score must be one of %s" % sorted(MOE_SCORES))
     if not 1 <= top_k <= E:
         raise ValueError("top_k must be 1 .. %d (the experts), got %d" % (E, top_k))
-    f32, i32 = torch.float32, torch.int32
-    _dense(bias, (E,), f32, dev, "bias")
+    f32, i32, empty, L = torch.float32, torch.int32, torch.empty, lib()
+    bias_p = _dense(bias, (E,), f32, dev, "bias")
+    _dense(weights, (T, top_k), f32, dev, "weights")
+    _dense(experts, (T, top_k), i32, dev, "experts")
+    _dense(offsets, (E + 1,), i32, dev, "offsets")
+    _dense(row_token, (T * top_k,), i32, dev, "row_token")
+    _dense(token_row, (T, top_k), i32, dev, "token_row")
+    ws_p, wsb = None, 0
     with _scope(dev, stream):
-        weights = _out(weights, (T, top_k), f32, dev, "weights")
-        experts = _out(experts, (T, top_k), i32, dev, "experts")
-        offsets = _out(offsets, (E + 1,), i32, dev, "offsets")
-        row_token = _out(row_token, (T * top_k,), i32, dev, "row_token")
-        token_row = _out(token_row, (T, top_k), i32, dev, "token_row")
-        need = moe_route_workspace_size(T, E, top_k)
-        if workspace is None and need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
-        _check(lib().sq_moe_route(_ptr(logits), _dtype_code(logits), T, E, ld, top_k,
-                                  MOE_SCORES[score], _ptr(bias), int(renormalize), scale,
-                                  _ptr(weights), _ptr(experts), _ptr(offsets), _ptr(row_token),
-                                  _ptr(token_row), _ptr(workspace), wsb, _stream(stream)),
-               "sq_moe_route")
+        if weights is None:
+            weights = empty(T, top_k, dtype=f32, device=dev)
+        if experts is None:
+            experts = empty(T, top_k, dtype=i32, device=dev)
+        if offsets is None:
+            offsets = empty(E + 1, dtype=i32, device=dev)
+        if row_token is None:
+            row_token = empty(T * top_k, dtype=i32, device=dev)
+        if token_row is None:
+            token_row = empty(T, top_k, dtype=i32, device=dev)
+        if workspace is None:
+            need = L.sq_moe_route_workspace_size(T, E, top_k)
+            if need:
+                workspace = empty(need, dtype=torch.uint8, device=dev)
+        if workspace is not None:
+            if workspace.device != dev or not workspace.is_contiguous():
+                raise ValueError("workspace must be contiguous and on the device of logits")
+            ws_p, wsb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        _check(L.sq_moe_route(logits.data_ptr(), _dtype_code(logits), T, E, ld, top_k,
+                              MOE_SCORES[score], bias_p, int(renormalize), scale,
+                              weights.data_ptr(), experts.data_ptr(), offsets.data_ptr(),
+                              row_token.data_ptr(), token_row.data_ptr(), ws_p, wsb,
+                              _raw_stream(dev.index)), "sq_moe_route")
     return MoeRoute(weights, experts, offsets, row_token, token_row)
 
 
 def _gemm_grouped(call: str, code: torch.dtype, raw: str, Xq, Wq, x_scale, w_scale, offsets,
                   row_token, epi, out, path_hint, stream):
+    dev = Xq.device
     if Xq.dim() != 2 or Wq.dim() != 3 or Wq.shape[2] != Xq.shape[1] or Xq.dtype != code \
             or Wq.dtype != code or not Xq.is_contiguous() or not Wq.is_contiguous() \
-            or not Xq.is_cuda or Wq.device != Xq.device:
+            or not Xq.is_cuda or Wq.device != dev:
         raise ValueError("Xq [X,K] and Wq [E,N,K] must be contiguous %s tensors on one CUDA "
                          "device" % code)
     X, K = Xq.shape
     E, N, _ = Wq.shape
-    dev = Xq.device
     if epi not in ("bf16", "bf16_relu", raw):
         raise ValueError("epi must be bf16, bf16_relu or %s" % raw)
     want = torch.bfloat16 if epi != raw else torch.int32 if raw == "i32" else torch.float32
     R = X if row_token is None else row_token.numel()
-    _dense(offsets, (E + 1,), torch.int32, dev, "offsets")
-    _dense(row_token, (R,), torch.int32, dev, "row_token")
-    _dense(x_scale, (X,), torch.float32, dev, "x_scale")
-    _dense(w_scale, (E, N), torch.float32, dev, "w_scale")
+    off_p = _dense(offsets, (E + 1,), torch.int32, dev, "offsets")
+    row_p = _dense(row_token, (R,), torch.int32, dev, "row_token")
+    xs_p = _dense(x_scale, (X,), torch.float32, dev, "x_scale")
+    ws_p = _dense(w_scale, (E, N), torch.float32, dev, "w_scale")
+    L = lib()
     with _scope(dev, stream):
+        ldo = N
         if out is None:
-            out = torch.empty((R, N), dtype=want, device=dev)
+            out = torch.empty(R, N, dtype=want, device=dev)
         elif (out.dim() != 2 or out.shape != (R, N) or out.dtype != want or out.device != dev
               or (N > 1 and out.stride(1) != 1) or (R > 1 and out.stride(0) < N)):
             raise ValueError("out must be a [R, N] = [%d, %d] %s tensor with unit column stride "
                              "on the device of Xq" % (R, N, want))
-        ldo = out.stride(0) if R > 1 else max(N, 1)
-        _check(getattr(lib(), call)(_ptr(Xq), X, _ptr(Wq), _ptr(x_scale), _ptr(w_scale),
-                                    _ptr(offsets), _ptr(row_token), R, E, N, K, EPI[epi],
-                                    _ptr(out), ldo, path_hint, _stream(stream)), call)
+        elif R > 1:
+            ldo = out.stride(0)
+        _check(getattr(L, call)(Xq.data_ptr(), X, Wq.data_ptr(), xs_p, ws_p, off_p, row_p, R, E, N,
+                                K, EPI[epi], out.data_ptr(), ldo, path_hint,
+                                _raw_stream(dev.index)), call)
     return out
 
 
@@ -793,45 +813,55 @@ def block_norm_quant_per_token(x: torch.Tensor, residual: Optional[torch.Tensor]
     the experts' rows [R, K] and each token's are summed first.  ``h_out`` may be
     ``residual`` itself; without ``quant`` only h is computed (None, None)."""
     R, K, ldx = _rows(x, "x")
-    dev, dt = x.device, x.dtype
-    a = BlockNormArgs()
-    a.dtype = _dtype_code(x)
-    M, top_k = R, 0
+    dev, dt, f32, empty = x.device, x.dtype, torch.float32, torch.empty
+    M, top_k, row_p, w_p = R, 0, None, None
     if (token_row is None) != (weights is None):
         raise ValueError("token_row and weights go together")
     if token_row is not None:
         if token_row.dim() != 2:
             raise ValueError("token_row must be [M, top_k]")
         M, top_k = token_row.shape
-        a.token_row = _dense(token_row, (M, top_k), torch.int32, dev, "token_row").data_ptr()
-        a.weights = _dense(weights, (M, top_k), torch.float32, dev, "weights").data_ptr()
-    a.x, a.ldx, a.R, a.top_k, a.M, a.K = x.data_ptr(), ldx, R, top_k, M, K
-    for name, v, n in (("post_gamma", post_gamma, K), ("post_beta", post_beta, K),
-                       ("gate", gate, K), ("token_gate", token_gate, M),
-                       ("pre_gamma", pre_gamma, K), ("pre_beta", pre_beta, K)):
-        if v is not None:
-            setattr(a, name, _dense(v, (n,), torch.float32, dev, name).data_ptr())
-    a.post_norm, a.post_eps, a.pre_norm, a.pre_eps = post_norm, post_eps, pre_norm, pre_eps
+        row_p = _dense(token_row, (M, top_k), torch.int32, dev, "token_row")
+        w_p = _dense(weights, (M, top_k), f32, dev, "weights")
+    vec = (K,)
+    post_g = _dense(post_gamma, vec, f32, dev, "post_gamma")
+    post_b = _dense(post_beta, vec, f32, dev, "post_beta")
+    gate_p = _dense(gate, vec, f32, dev, "gate")
+    token_p = _dense(token_gate, (M,), f32, dev, "token_gate")
+    pre_g = _dense(pre_gamma, vec, f32, dev, "pre_gamma")
+    pre_b = _dense(pre_beta, vec, f32, dev, "pre_beta")
+    res_p, ld_res, ld_h = None, K, K
     for name, v in (("residual", residual), ("h_out", h_out)):
         if v is not None and (v.shape != (M, K) or v.dtype != dt or v.device != dev):
             raise ValueError("%s must be [%d, %d] %s on the device of x" % (name, M, K, dt))
     if residual is not None:
-        a.residual, a.ld_res = residual.data_ptr(), _rows(residual, "residual")[2]
-    a.residual_scale = residual_scale
+        res_p, ld_res = residual.data_ptr(), _rows(residual, "residual")[2]
+    if h_out is not None:
+        ld_h = _rows(h_out, "h_out")[2]
+    code = torch.uint8 if fp8 else torch.int8
+    _dense(Xq, (M, K), code, dev, "Xq")
+    _dense(x_scale, (M,), f32, dev, "x_scale")
+    call = "sq_block_norm_quant_per_token_fp8" if fp8 else "sq_block_norm_quant_per_token"
+    L = lib()
     with _scope(dev, stream):
         if h_out is None:
-            h_out = torch.empty((M, K), dtype=dt, device=dev)
-        a.h_out, a.ld_h = h_out.data_ptr(), _rows(h_out, "h_out")[2]
+            h_out = empty(M, K, dtype=dt, device=dev)
+        q_p = s_p = None
         if quant:
-            Xq = _out(Xq, (M, K), torch.uint8 if fp8 else torch.int8, dev, "Xq")
-            x_scale = _out(x_scale, (M,), torch.float32, dev, "x_scale")
-            a.Xq, a.x_scale = Xq.data_ptr(), x_scale.data_ptr()
+            if Xq is None:
+                Xq = empty(M, K, dtype=code, device=dev)
+            if x_scale is None:
+                x_scale = empty(M, dtype=f32, device=dev)
+            q_p, s_p = Xq.data_ptr(), x_scale.data_ptr()
         else:
             Xq = x_scale = None
         if M == 0:
             return h_out, Xq, x_scale
-        call = "sq_block_norm_quant_per_token_fp8" if fp8 else "sq_block_norm_quant_per_token"
-        _check(getattr(lib(), call)(ctypes.byref(a), _stream(stream)), call)
+        a = BlockNormArgs(x.data_ptr(), ldx, R, row_p, w_p, top_k, _dtype_code(x), M, K, post_norm,
+                          post_g, post_b, post_eps, gate_p, token_p, res_p, ld_res,
+                          residual_scale, pre_norm, pre_g, pre_b, pre_eps, h_out.data_ptr(), ld_h,
+                          q_p, s_p)
+        _check(getattr(L, call)(ctypes.byref(a), _raw_stream(dev.index)), call)
     return h_out, Xq, x_scale
 
 
