@@ -5,9 +5,11 @@
 // registers (lane l the experts l, l + 32, ...), takes the largest key k
 // times with warp-wide integer maxima (keys are the logits' bits mapped to
 // order like integers, so a maximum costs one redux), and the lowest index
-// among equal keys with a warp-wide minimum.  A CTA walks a contiguous range
-// of tokens in groups of 64; within a group each expert keeps a 64-bit mask of
-// the tokens that chose it (a token chooses an expert at most once), so a
+// among equal keys with a warp-wide minimum; up to 128 experts a warp takes two
+// tokens at once, so that one's maxima are in flight behind the other's, and
+// sorts each lane's keys first, so that a choice looks at one of them.  A CTA
+// walks a contiguous range of tokens in groups of 64; within a group each expert
+// keeps a 64-bit mask of the tokens that chose it (a token chooses an expert at most once), so a
 // row's rank among the group's rows of that expert is a population count --
 // stable in token order whatever order the mask's atomics arrived in.  The
 // second pass adds, per expert, the counts of all earlier CTAs and experts and
@@ -26,10 +28,12 @@
 namespace sq {
 namespace {
 
-constexpr int kRouteThreads = 512;
+constexpr int kRouteThreads = 1024;
 constexpr int kRouteWarps = kRouteThreads / 32;
 constexpr int kGroup = 64;      // tokens of one mask
+constexpr int kPerWarp = kGroup / kRouteWarps;
 constexpr int kMaxBlocks = 148; // CTAs of the first pass: the second reads all their counts
+static_assert(kPerWarp == 2, "a warp ranks two tokens of a group");
 constexpr int kMaxExperts = SQ_MOE_MAX_EXPERTS;
 
 struct RouteParams {
@@ -65,94 +69,133 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t v) {
   return (static_cast<uint64_t>(hi) << 32) | __reduce_max_sync(~0u, lo);
 }
 
+// NaN and -inf (never chosen) become -inf, +inf the largest finite value, -0
+// becomes +0 (equal keys).
+__device__ __forceinline__ float clean_logit(float v) {
+  return v >= -FLT_MAX ? fminf(v, FLT_MAX) + 0.0f : -INFINITY;
+}
+
 __device__ __forceinline__ float sigmoid_f(float l) { return 1.0f / (1.0f + expf(-l)); }
 
 __device__ __forceinline__ float load_logit(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 __device__ __forceinline__ float load_logit(const float* p) { return *p; }
 
-// One token's choice by one warp: lane j < top_k returns its j-th expert (-1:
-// none left) and its weight.  V: experts per lane.  Key 0 marks an expert that
-// cannot be chosen (every finite value's key is above it).
-template <typename T, int V, bool kBias>
-__device__ __forceinline__ void choose(const RouteParams& p, int64_t t, int lane, int& my_e,
-                                       float& my_w) {
+// The choices of U tokens by one warp: lane j < top_k gets each token's j-th
+// expert (-1: none left, or no token) and its weight.  V: experts per lane.  Key 0 marks an
+// expert that cannot be chosen (every finite value's key is above it).
+template <typename T, int V, int U, bool kBias>
+__device__ __forceinline__ void choose(const RouteParams& p, const int64_t (&t)[U], int64_t t_end,
+                                       int lane, int (&my_e)[U], float (&my_w)[U]) {
   using Key = typename std::conditional<kBias, uint64_t, uint32_t>::type;
-  const T* row = static_cast<const T*>(p.logits) + t * p.ld;
-  float l[V];
-  Key key[V];
+  constexpr bool kSorted = V <= 4;
+  float l[U][V];
+  Key key[U][V];
+  int ex[U][V];  // the keys' experts
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = lane + 32 * i;
-    float v = -INFINITY;
-    if (e < p.E) v = load_logit(row + e);
-    if (!(v >= -FLT_MAX)) v = -INFINITY;  // NaN too
-    l[i] = fminf(v, FLT_MAX) + 0.0f;  // -0 becomes +0: the two are equal keys
-  }
-  float m = -FLT_MAX;
+  for (int u = 0; u < U; ++u) {
+    const T* row = static_cast<const T*>(p.logits) + t[u] * p.ld;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const bool ok = l[i] >= -FLT_MAX;
-    m = fmaxf(m, l[i]);
-    if constexpr (kBias) {
-      key[i] = 0;
-      if (ok) {
-        const double s = 1.0 / (1.0 + exp(-static_cast<double>(l[i]))) +
-                         static_cast<double>(p.bias[lane + 32 * i]) + 0.0;
-        if (s > -INFINITY) key[i] = order_key(s);  // false for NaN
-      }
-    } else {
-      key[i] = ok ? order_key(l[i]) : 0;
+    for (int i = 0; i < V; ++i) {
+      const int e = lane + 32 * i;
+      l[u][i] = -INFINITY;
+      if (t[u] < t_end && e < p.E) l[u][i] = load_logit(row + e);
     }
   }
-  float total = 0.0f;
-  if (!p.sigmoid) {
-    // the row's maximum through the order-preserving keys
-    const uint32_t mk = __reduce_max_sync(~0u, order_key(m));
-    m = __uint_as_float((mk & 0x80000000u) ? (mk ^ 0x80000000u) : ~mk);
-    if (!p.renorm) {
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (l[i] >= -FLT_MAX) total += expf(l[i] - m);
+  for (int u = 0; u < U; ++u) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float v = l[u][i] = clean_logit(l[u][i]);
+      ex[u][i] = lane + 32 * i;
+      key[u][i] = 0;
+      if (v >= -FLT_MAX) {
+        if constexpr (kBias) {
+          const double s = 1.0 / (1.0 + exp(-static_cast<double>(v))) +
+                           static_cast<double>(p.bias[lane + 32 * i]) + 0.0;
+          if (s > -INFINITY) key[u][i] = order_key(s);  // false for NaN
+        } else {
+          key[u][i] = order_key(v);
+        }
+      }
+    }
+    if constexpr (kSorted) {  // adjacent exchanges: equal keys keep their order
+#pragma unroll
+      for (int a = 0; a < V - 1; ++a)
+#pragma unroll
+        for (int b = 0; b < V - 1 - a; ++b) {
+          const bool swap = key[u][b + 1] > key[u][b];
+          const Key k = key[u][b];
+          const int e = ex[u][b];
+          key[u][b] = swap ? key[u][b + 1] : k;
+          ex[u][b] = swap ? ex[u][b + 1] : e;
+          key[u][b + 1] = swap ? k : key[u][b + 1];
+          ex[u][b + 1] = swap ? e : ex[u][b + 1];
+        }
+    }
+    my_e[u] = -1;
+  }
+  for (int j = 0; j < p.top_k; ++j) {
+    Key best[U], top[U];
+    int at[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      best[u] = key[u][0];
+      at[u] = ex[u][0];
+      if constexpr (!kSorted) {
+#pragma unroll
+        for (int i = 1; i < V; ++i)  // ascending index: the first of equal keys stays
+          if (key[u][i] > best[u]) {
+            best[u] = key[u][i];
+            at[u] = ex[u][i];
+          }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) top[u] = warp_max(best[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool wins = top[u] != 0 && best[u] == top[u];  // 0: nothing left to choose
+      const int e = static_cast<int>(
+          __reduce_min_sync(~0u, static_cast<uint32_t>(wins ? at[u] : kMaxExperts)));
+      if (lane == j && e < kMaxExperts) my_e[u] = e;
+      if constexpr (kSorted) {
+        if (wins && at[u] == e) {  // the winner's list moves up
+#pragma unroll
+          for (int i = 0; i + 1 < V; ++i) {
+            key[u][i] = key[u][i + 1];
+            ex[u][i] = ex[u][i + 1];
+          }
+          key[u][V - 1] = 0;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (e == ex[u][i]) key[u][i] = 0;
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    float mine = 0.0f;  // the chosen logit, from L1
+    if (my_e[u] >= 0)
+      mine = clean_logit(load_logit(static_cast<const T*>(p.logits) + t[u] * p.ld + my_e[u]));
+    const float m = __shfl_sync(~0u, mine, 0);  // softmax: the first choice is the largest
+    my_w[u] = 0.0f;
+    if (my_e[u] >= 0) my_w[u] = p.sigmoid ? sigmoid_f(mine) : expf(mine - m);
+    float total = 1.0f;
+    if (p.renorm || !p.sigmoid) {
+      total = my_w[u];
+      if (!p.renorm) {
+        total = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (l[u][i] >= -FLT_MAX) total += expf(l[u][i] - m);
+      }
 #pragma unroll
       for (int s = 16; s > 0; s >>= 1) total += __shfl_xor_sync(~0u, total, s);
     }
+    my_w[u] = total > 0.0f ? my_w[u] / total * p.scale : 0.0f;
   }
-  my_e = -1;
-  my_w = 0.0f;
-  float my_l = 0.0f;
-  for (int j = 0; j < p.top_k; ++j) {
-    Key best = 0;
-    int at = kMaxExperts;
-    float lv = 0.0f;
-#pragma unroll
-    for (int i = 0; i < V; ++i)  // ascending index: the first of equal keys stays
-      if (key[i] > best) {
-        best = key[i];
-        at = lane + 32 * i;
-        lv = l[i];
-      }
-    const Key top = warp_max(best);
-    if (top == 0) break;  // nothing left to choose
-    const int e = static_cast<int>(
-        __reduce_min_sync(~0u, static_cast<uint32_t>(best == top ? at : kMaxExperts)));
-    lv = __shfl_sync(~0u, lv, e & 31);
-    if (lane == j) {
-      my_e = e;
-      my_l = lv;
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (e == lane + 32 * i) key[i] = 0;
-  }
-  if (my_e >= 0) my_w = p.sigmoid ? sigmoid_f(my_l) : expf(my_l - m);
-  if (p.renorm) {
-    total = my_w;
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) total += __shfl_xor_sync(~0u, total, s);
-  } else if (p.sigmoid) {
-    total = 1.0f;
-  }
-  my_w = total > 0.0f ? my_w / total * p.scale : 0.0f;
 }
 
 // Exclusive prefix sum of counts[0 .. E) into offsets[0 .. E] (shared memory),
@@ -182,38 +225,44 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const RoutePar
   const int64_t t_begin = static_cast<int64_t>(blockIdx.x) * p.per_block;
   const int64_t t_end = min(p.T, t_begin + p.per_block);
   for (int e = threadIdx.x; e < p.E; e += kRouteThreads) count[e] = 0;
+  // the second pass may be scheduled now; it waits for this grid before it reads
+  if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   for (int64_t g = t_begin; g < t_end; g += kGroup) {
     for (int e = threadIdx.x; e < p.E; e += kRouteThreads) mask[e] = 0;
     __syncthreads();
-    int my_e[kGroup / kRouteWarps];
+    const int64_t t[kPerWarp] = {g + warp, g + warp + kRouteWarps};
+    int my_e[kPerWarp];
+    float w[kPerWarp];
+    if constexpr (V <= 4) {
+      choose<T, V, kPerWarp, kBias>(p, t, t_end, lane, my_e, w);
+    } else {  // registers: one token after the other
 #pragma unroll
-    for (int i = 0; i < kGroup / kRouteWarps; ++i) {
-      const int64_t t = g + warp + i * kRouteWarps;
-      my_e[i] = -1;
-      if (t < t_end) {
-        float w;
-        choose<T, V, kBias>(p, t, lane, my_e[i], w);
-        if (lane < p.top_k) {
-          p.weights[t * p.top_k + lane] = w;
-          p.experts[t * p.top_k + lane] = my_e[i];
-          if (my_e[i] >= 0) atomicOr(&mask[my_e[i]], 1ull << (warp + i * kRouteWarps));
-        }
+      for (int u = 0; u < kPerWarp; ++u) {
+        const int64_t one[1] = {t[u]};
+        int e1[1];
+        float w1[1];
+        choose<T, V, 1, kBias>(p, one, t_end, lane, e1, w1);
+        my_e[u] = e1[0];
+        w[u] = w1[0];
       }
     }
+#pragma unroll
+    for (int u = 0; u < kPerWarp; ++u)
+      if (t[u] < t_end && lane < p.top_k) {
+        p.weights[t[u] * p.top_k + lane] = w[u];
+        p.experts[t[u] * p.top_k + lane] = my_e[u];
+        if (my_e[u] >= 0) atomicOr(&mask[my_e[u]], 1ull << (warp + u * kRouteWarps));
+      }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kGroup / kRouteWarps; ++i) {
-      const int tl = warp + i * kRouteWarps;
-      const int64_t t = g + tl;
-      if (t < t_end && lane < p.top_k) {
+    for (int u = 0; u < kPerWarp; ++u)
+      if (t[u] < t_end && lane < p.top_k) {
         // the row's rank among this CTA's rows of its expert
-        const int r = my_e[i] < 0
-                          ? -1
-                          : count[my_e[i]] + __popcll(mask[my_e[i]] & ((1ull << tl) - 1));
-        p.token_row[t * p.top_k + lane] = r;
+        const unsigned long long before = (1ull << (warp + u * kRouteWarps)) - 1ull;
+        p.token_row[t[u] * p.top_k + lane] =
+            my_e[u] < 0 ? -1 : count[my_e[u]] + __popcll(mask[my_e[u]] & before);
       }
-    }
     __syncthreads();
     for (int e = threadIdx.x; e < p.E; e += kRouteThreads) count[e] += __popcll(mask[e]);
   }
@@ -244,15 +293,22 @@ __global__ void __launch_bounds__(kRouteThreads) moe_scatter_kernel(const RouteP
   __shared__ int off[kMaxExperts + 1];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int b = static_cast<int>(blockIdx.x);
-  for (int e = threadIdx.x; e < p.E; e += kRouteThreads) {
+  for (int e = threadIdx.x; e < p.E; e += kRouteThreads) before[e] = total[e] = 0;
+  __syncthreads();
+  // the counts of all CTAs of the first pass, the threads of an expert taking
+  // every parts-th of them, eight loads in flight each
+  const int parts = max(1, kRouteThreads / p.E);
+  for (int i = threadIdx.x; i < parts * p.E; i += kRouteThreads) {
+    const int e = i % p.E;
     int s = 0, all = 0;
-    for (int i = 0; i < p.blocks; ++i) {
-      const int c = p.hist[static_cast<int64_t>(i) * p.E + e];
-      if (i < b) s += c;
+#pragma unroll 8
+    for (int k = i / p.E; k < p.blocks; k += parts) {
+      const int c = __ldcg(p.hist + static_cast<int64_t>(k) * p.E + e);
+      if (k < b) s += c;
       all += c;
     }
-    before[e] = s;
-    total[e] = all;
+    atomicAdd(&before[e], s);
+    atomicAdd(&total[e], all);
   }
   __syncthreads();
   if (threadIdx.x < 32) scan_offsets(total, off, p.E, static_cast<int>(threadIdx.x));
@@ -266,7 +322,7 @@ __global__ void __launch_bounds__(kRouteThreads) moe_scatter_kernel(const RouteP
     if (e >= 0) {
       const int r = off[e] + before[e] + p.token_row[i];
       p.token_row[i] = r;
-      p.row_token[r] = static_cast<int>(i / p.top_k);
+      p.row_token[r] = static_cast<int>(static_cast<uint32_t>(i) / static_cast<uint32_t>(p.top_k));
     }
     if (i >= off[p.E]) p.row_token[i] = -1;  // behind the last expert's rows
   }
