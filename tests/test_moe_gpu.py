@@ -407,3 +407,245 @@ def test_block_norm_without_codes():
     h, q, s = sq.block_norm_quant_per_token(x, res, residual_scale=2.0, quant=False)
     assert q is None and s is None
     assert torch.equal(h, torch.addcmul(x, res, torch.full_like(res, 2.0)))  # 2 res is exact
+
+
+# ---------------------------------------------------------------------------
+# limits, streams, graphs, the layer
+# ---------------------------------------------------------------------------
+
+def test_grouped_equals_the_dense_gemm_of_each_expert():
+    rng = _rng(31)
+    counts, N, K = [300, 0, 5, 129], 520, 1040
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    xq, wq = _cuda_of(_codes(rng, (off[-1], K), False)), _cuda_of(_codes(rng, (4, N, K), False))
+    xs, ws = torch.rand(int(off[-1]), device="cuda"), torch.rand((4, N), device="cuda")
+    for epi in ("bf16", "bf16_relu"):
+        for path in (1, 2):
+            got = sq.w8a8_gemm_grouped(xq, wq, xs, ws, _cuda_of(off), epi=epi, path_hint=path)
+            for e in range(4):
+                if counts[e]:
+                    sl = slice(int(off[e]), int(off[e + 1]))
+                    one = sq.w8a8_gemm_dequant(xq[sl].clone(), wq[e], xs[sl].clone(), ws[e].clone(), epi)
+                    assert torch.equal(got[sl], one)
+
+
+@pytest.mark.parametrize("path", [1, 2])
+@pytest.mark.parametrize("gather", [False, True])
+def test_grouped_wait_limit(path, gather):
+    """A wait that runs out is an error status, and the next call is right."""
+    rng = _rng(32)
+    counts, N, K, X = [200, 300], 700, 2048, 500
+    off = _cuda_of(np.array([0, 200, 500], np.int32))
+    row = _cuda_of(rng.permutation(X).astype(np.int32)) if gather else None
+    xq, wq = _cuda_of(_codes(rng, (X, K), False)), _cuda_of(_codes(rng, (2, N, K), False))
+    call = lambda: sq.w8a8_gemm_grouped(xq, wq, None, None, off, row_token=row, epi="i32", path_hint=path)  # noqa: E731
+    want = call()
+    torch.cuda.synchronize()
+    assert sq.get_device_error() == 0
+    sq.set_wait_limit(1)
+    try:
+        call()
+        assert sq.status_string(sq.get_device_error()).startswith("SQ_ERR_PIPELINE_TIMEOUT")
+    finally:
+        sq.set_wait_limit(0)
+    assert torch.equal(call(), want)
+    assert sq.get_device_error() == 0
+
+
+def test_block_norm_after_a_wait_limit():
+    """One probe of a barrier may sleep until its row has landed, so a budget of one may or may
+    not run out; either way the call returns, and the next one is right."""
+    x = torch.randn((4000, 4096), device="cuda").to(torch.bfloat16)
+    res = torch.randn_like(x)
+    want = sq.block_norm_quant_per_token(x, res, post_norm=sq.NORM_RMS)
+    sq.set_wait_limit(1)
+    try:
+        sq.block_norm_quant_per_token(x, res, post_norm=sq.NORM_RMS)
+        assert sq.get_device_error() in (0, 6)  # SQ_OK, SQ_ERR_PIPELINE_TIMEOUT
+    finally:
+        sq.set_wait_limit(0)
+    for a, b in zip(sq.block_norm_quant_per_token(x, res, post_norm=sq.NORM_RMS), want):
+        assert torch.equal(a, b)
+    assert sq.get_device_error() == 0
+
+
+def test_block_norm_pipeline_equals_the_single_row_kernel():
+    """The rows of a large batch (pipelined) against the same rows in batches
+    too small for the pipeline: the same values, sums in another order."""
+    x = torch.randn((8000, 1040), device="cuda")
+    res = torch.randn_like(x)
+    rows = torch.randint(-1, 8000, (5000, 3), device="cuda", dtype=torch.int32)
+    w = torch.rand((5000, 3), device="cuda")
+    g = torch.rand(1040, device="cuda")
+    kw = dict(post_norm=sq.NORM_LAYER, post_gamma=g, gate=g, pre_gamma=g)
+    h, q, s = sq.block_norm_quant_per_token(x, res[:5000], token_row=rows, weights=w, **kw)
+    h1, q1, s1 = sq.block_norm_quant_per_token(x, res[:100], token_row=rows[:100].contiguous(),
+                                               weights=w[:100].contiguous(), **kw)
+    # both within 300 roundings of the same number (|h| of order 1)
+    assert (h[:100] - h1).abs().max() <= 300 * 2.0 ** -24 * max(1.0, float(h1.abs().max()))
+    assert (q[:100].int() - q1.int()).abs().max() <= 1
+
+
+def _layer(fmt, T=70, E=8, H=256, I=160, top_k=2, seed=0, **kw):
+    from w8a8_int8_quantized_norm_b200 import moe
+
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+    rand = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    gu, dn = (rand(E, 2 * I, H) * 0.05).to(torch.bfloat16), (rand(E, H, I) * 0.05).to(torch.bfloat16)
+    x, res = rand(T, H).to(torch.bfloat16), rand(T, H).to(torch.bfloat16)
+    x[:, 3] *= 40
+    gamma = torch.rand(H, device="cuda", generator=gen) + 0.5
+    layer = moe.MoELayer(gu, dn, top_k, fmt=fmt, **kw)
+    act = sq.calibrate_absmax(x, sq.NORM_RMS, gamma)
+    layer.prepare(act, 0.5, gamma)
+    norm = sq.norm_smooth_quant_per_token if fmt == "int8" else sq.norm_smooth_quant_per_token_fp8
+    logits = rand(T, E)
+    Xq, xs = norm(x, sq.NORM_RMS, layer.gamma)
+    block = dict(post_norm=sq.NORM_RMS, post_gamma=gamma, pre_norm=sq.NORM_RMS, pre_gamma=gamma,
+                 residual_scale=0.5)
+    return layer, x, gamma, Xq, xs, logits, res, block
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp8"])
+def test_layer_stage_by_stage(fmt):
+    import oracle
+
+    layer, x, gamma, Xq, xs, logits, res, block = _layer(fmt)
+    logits[60:] = -float("inf")  # a padded tail
+    h, q, s = layer.forward(Xq, xs, logits, res, **block)
+    st = layer.stages
+    w, e, off, row, tok, bound = ref.route(_np64(logits), 2)
+    r = st["route"]
+    for got, want in ((r.experts, e), (r.offsets, off), (r.row_token, row), (r.token_row, tok)):
+        assert np.array_equal(got.cpu().numpy(), want)
+    n = int(off[-1])
+    fp8 = fmt == "fp8"
+    a = _values(Xq.cpu().numpy(), fp8) * _np64(xs)[:, None]
+    wide = _values(layer.gate_up_q.cpu().numpy(), fp8) * _np64(layer.gate_up_scale)[:, :, None]
+    narrow = _values(layer.down_q.cpu().numpy(), fp8) * _np64(layer.down_scale)[:, :, None]
+    ha = _values(st["Hq"].cpu().numpy(), fp8) * _np64(st["h_scale"])[:, None]
+    gu, y = _np64(st["gate_up"]), _np64(st["down"])
+    for ex in range(8):
+        sl = slice(off[ex], off[ex + 1])
+        for got, left, right in ((gu[sl], a[row[sl]], wide[ex]), (y[sl], ha[sl], narrow[ex])):
+            want = left @ right.T
+            # accumulation (FP8) and the two scales' roundings, then bf16's half step
+            slack = (31 + 8 + 4) * 2.0 ** -23 * (np.abs(left) @ np.abs(right).T)
+            assert (np.abs(got - want) <= slack + 2.0 ** -8 * (np.abs(want) + slack)).all()
+    if not fp8:
+        bits = st["gate_up"][:n].view(torch.int16).cpu().numpy().view(np.uint16)
+        hq, hs, _ = oracle.silu_mul_quant(bits)
+        assert np.array_equal(st["Hq"][:n].cpu().numpy(), hq)
+        assert np.array_equal(st["h_scale"][:n].cpu().numpy(), hs)
+    g = gamma.cpu().numpy()
+    hr, dh, yr, dy = ref.block_norm(y, _np64(res), tok, r.weights.cpu().numpy().astype(np.float64),
+                                    ("rms", g, None, 1e-5), None, None, 0.5, ("rms", g, None, 1e-5))
+    assert (np.abs(_np64(h) - hr) <= dh + 2.0 ** -8 * (np.abs(hr) + dh)).all()
+    vals = _values(q.cpu().numpy(), fp8)
+    ref.check_codes(vals, _np64(s), yr, dy, 448.0 if fp8 else 127.0)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp8"])
+def test_layer_is_near_the_unquantised_experts(fmt):
+    """The whole layer against fp64 experts on the bf16 weights: smoothed 8-bit codes keep the
+    sum of the experts within a few percent (a wrong fold, expert or weight is far outside)."""
+    layer, x, gamma, Xq, xs, logits, res, _ = _layer(fmt, T=64)
+    h, _, _ = layer.forward(Xq, xs, logits, None, post_norm=sq.NORM_NONE, quant=False)
+    X = _np64(x)
+    n = X / np.sqrt((X * X).mean(1, keepdims=True) + 1e-5) * gamma.cpu().numpy()
+    w, e, *_ = ref.route(_np64(logits), 2)
+    gu, dn = _np64(layer.gate_up), _np64(layer.down)
+    want = np.zeros_like(X)
+    for t in range(64):
+        for j in range(2):
+            z = gu[e[t, j]] @ n[t]
+            g, u = z[:160], z[160:]
+            want[t] += w[t, j] * (dn[e[t, j]] @ (g / (1 + np.exp(-g)) * u))
+    rel = np.linalg.norm(_np64(h) - want) / np.linalg.norm(want)
+    # int8: four roundings of about step / sqrt(12), step = max / 127; e4m3: 2^-4 / sqrt(3) each
+    assert rel < (0.05 if fmt == "int8" else 0.12)
+
+
+def test_layer_in_a_graph_and_on_another_stream():
+    layer, x, gamma, Xq, xs, logits, res, block = _layer("int8", T=33)
+    want = [t.clone() for t in layer.forward(Xq, xs, logits, res, **block)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = layer.forward(Xq, xs, logits, res, stream=side, **block)
+    side.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    # two captured graphs, replayed in turn on changed inputs
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = layer.forward(Xq, xs, logits, res, **block)
+        graphs.append((g, out))
+    logits.copy_(logits.flip(0))
+    fresh = [t.clone() for t in layer.forward(Xq, xs, logits, res, **block)]
+    for g, out in graphs + graphs[:1]:
+        for t in out:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, fresh):
+            assert torch.equal(a, b)
+
+
+def test_calls_on_two_streams_at_once():
+    """No call shares scratch with another: two streams at once give what each gives alone."""
+    logits = [torch.randn((5000, 64), device="cuda") for _ in range(2)]
+    x = [torch.randn((4000, 2048), device="cuda").to(torch.bfloat16) for _ in range(2)]
+    alone = [(sq.moe_route(l, 6), sq.block_norm_quant_per_token(v, v)) for l, v in zip(logits, x)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(10):
+        for i, st in enumerate(streams):
+            got[i].append((sq.moe_route(logits[i], 6, stream=st),
+                           sq.block_norm_quant_per_token(x[i], x[i], stream=st)))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for r, b in got[i]:
+            for u, v in zip(tuple(r) + tuple(b), tuple(alone[i][0]) + tuple(alone[i][1])):
+                assert torch.equal(u, v)
+
+
+def test_binding_refusals():
+    x = torch.randn((4, 64), device="cuda")
+    with pytest.raises(ValueError):
+        sq.moe_route(x, 65)
+    with pytest.raises(ValueError):
+        sq.moe_route(x, 2, score="relu")
+    with pytest.raises(ValueError):
+        sq.moe_route(x, 2, score="sigmoid", bias=torch.zeros(63, device="cuda"))
+    with pytest.raises(sq.SQError):
+        sq.moe_route(x, 2, bias=torch.zeros(64, device="cuda"))  # softmax takes none
+    with pytest.raises(sq.SQError):
+        sq.moe_route(torch.randn((100, 64), device="cuda"), 2,
+                     workspace=torch.empty(4, dtype=torch.uint8, device="cuda"))
+    codes, w = torch.zeros((4, 64), dtype=torch.int8, device="cuda"), \
+        torch.zeros((2, 8, 64), dtype=torch.int8, device="cuda")
+    off = torch.zeros(3, dtype=torch.int32, device="cuda")
+    ok = (torch.zeros(4, device="cuda"), torch.zeros((2, 8), device="cuda"))
+    with pytest.raises(ValueError):
+        sq.w8a8_gemm_grouped(codes, w, *ok, off.long())
+    with pytest.raises(ValueError):
+        sq.w8a8_gemm_grouped(codes, w, *ok, off[:2])
+    with pytest.raises(ValueError):
+        sq.w8a8_gemm_grouped(codes, w, *ok, off, out=torch.zeros((4, 9), dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(ValueError):
+        sq.w8a8_gemm_grouped(codes.view(torch.uint8), w, *ok, off)
+    with pytest.raises(sq.SQError):
+        sq.w8a8_gemm_grouped(codes, w, None, None, off)  # bf16 needs scales
+    with pytest.raises(ValueError):
+        sq.block_norm_quant_per_token(x, token_row=torch.zeros((4, 2), dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError):
+        sq.block_norm_quant_per_token(x, x.double())
+    with pytest.raises(sq.SQError):
+        sq.block_norm_quant_per_token(x, h_out=x, token_row=torch.zeros((4, 1), dtype=torch.int32, device="cuda"),
+                                      weights=torch.zeros((4, 1), device="cuda"))
+    with pytest.raises(sq.SQError):
+        sq.block_norm_quant_per_token(torch.zeros((4, 72), device="cuda"))  # K % 16
