@@ -703,9 +703,10 @@ sq_status sq_moe_route(const void* logits, sq_dtype dtype, int64_t T, int64_t E,
  *   Xq       device [X, K] int8 (stride K); without row_token X >= R
  *   Wq       device [E, N, K] int8 (dense);  w_scale device [E, N] fp32
  *   x_scale  device [X] fp32 (both scales ignored for SQ_EPI_I32_RAW)
- *   offsets  device [E + 1] int32, ascending (sq_moe_route's); values are
- *            clamped to [0, R].  The group sizes stay on the device: nothing
- *            is read back, and an empty expert's weights are not read
+ *   offsets  device [E + 1] int32, ascending (sq_moe_route's); others count as
+ *            their running maximum within [0, R].  The group sizes stay on the
+ *            device: nothing is read back, and an empty expert's weights are
+ *            not read
  *   row_token  device [R] int32 or NULL; a row whose token is outside [0, X)
  *            is a row of zeros
  *   epi      SQ_EPI_BF16, SQ_EPI_BF16_RELU or SQ_EPI_I32_RAW
@@ -749,7 +750,8 @@ sq_status sq_fp8_gemm_grouped(const uint8_t* Xq8, int64_t X, const uint8_t* Wq8,
  * too; h is not rounded before pre_norm reads it; LayerNorm's variance is
  * taken around the mean).  The order of every sum depends on K and top_k
  * alone, or on M as well through the launch shape; it never depends on timing.
- * A row with a NaN or an infinity gets a non-finite x_scale.
+ * A row with a NaN or an infinity gets a non-finite x_scale.  A weight counts
+ * as it is: 0 times an infinity is a NaN (an entry outside [0, R) is not).
  */
 typedef struct sq_block_norm_args {
   const void* x;            /* device [R, K] (R = M without token_row), stride ldx */

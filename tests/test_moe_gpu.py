@@ -266,6 +266,30 @@ def test_grouped_bad_rows_and_offsets(path):
                          _cuda_of(np.array([20, 10, 5, 0], np.int32)), row_token=_cuda_of(row),
                          epi="i32", out=keep, path_hint=path)
     assert (keep == 5).all()
+    # groups that would overlap: the later one starts where the earlier ended
+    out = sq.w8a8_gemm_grouped(_cuda_of(xq), _cuda_of(wq), None, None,
+                               _cuda_of(np.array([0, 20, 10, 30], np.int32)), row_token=_cuda_of(row),
+                               epi="i32", path_hint=path).cpu().numpy()
+    assert np.array_equal(out[:20], a[:20] @ wq[0].astype(np.int64).T)
+    assert np.array_equal(out[20:], a[20:] @ wq[2].astype(np.int64).T)
+
+
+@pytest.mark.parametrize("path", [1, 2])
+def test_grouped_running_maximum_crosses_the_warp(path):
+    """More experts than a warp has lanes, with offsets that fall back in between."""
+    rng = _rng(14)
+    E, N, K, R = 70, 40, 64, 200
+    off = np.sort(rng.integers(0, R + 1, E + 1)).astype(np.int32)
+    off[[10, 33, 40, 64]] = [0, 3, 199, 1]
+    run = np.maximum.accumulate(np.clip(off, 0, R))
+    xq, wq = _codes(rng, (R, K), False), _codes(rng, (E, N, K), False)
+    out = torch.full((R, N), 5, dtype=torch.int32, device="cuda")
+    sq.w8a8_gemm_grouped(_cuda_of(xq), _cuda_of(wq), None, None, _cuda_of(off), epi="i32", out=out,
+                         path_hint=path)
+    want = np.full((R, N), 5, np.int64)
+    for e in range(E):
+        want[run[e]:run[e + 1]] = xq[run[e]:run[e + 1]].astype(np.int64) @ wq[e].astype(np.int64).T
+    assert np.array_equal(out.cpu().numpy(), want)
 
 
 # ---------------------------------------------------------------------------
@@ -565,6 +589,19 @@ def test_layer_is_near_the_unquantised_experts(fmt):
     rel = np.linalg.norm(_np64(h) - want) / np.linalg.norm(want)
     # int8: four roundings of about step / sqrt(12), step = max / 127; e4m3: 2^-4 / sqrt(3) each
     assert rel < (0.05 if fmt == "int8" else 0.12)
+
+
+def test_layer_without_tokens():
+    layer, x, gamma, Xq, xs, logits, res, block = _layer("int8", T=4)
+    h, q, s = layer.forward(Xq[:0], xs[:0], logits[:0], res[:0], **block)
+    assert h.shape == (0, 256) and q.shape == (0, 256) and s.shape == (0,)
+
+
+def test_layer_with_every_token_masked():
+    layer, x, gamma, Xq, xs, logits, res, block = _layer("int8", T=40)
+    logits.fill_(-float("inf"))
+    h, q, s = layer.forward(Xq, xs, logits, res, **dict(block, post_norm=sq.NORM_NONE, post_gamma=None))
+    assert torch.equal(h, (res.float() * 0.5).to(torch.bfloat16))
 
 
 def test_layer_in_a_graph_and_on_another_stream():

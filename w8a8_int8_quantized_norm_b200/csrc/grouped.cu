@@ -99,17 +99,27 @@ __device__ __forceinline__ int tiles_of(int count) {
   return (count + Cfg<kPair>::QT - 1) / Cfg<kPair>::QT;
 }
 
-// The table, by one warp; returns the number of entries (in every lane).
+// The table, by one warp; returns the number of entries (in every lane).  The
+// offsets count as their running maximum within [0, R]: whatever they hold, no
+// two groups share a row and the tiles are no more than the host allowed for.
 template <bool kPair>
 __device__ int build_table(const GroupedParams& p, Entry* table, int lane) {
-  int entries = 0, units = 0;
+  int entries = 0, units = 0, reached = 0;
   for (int e0 = 0; e0 < p.E; e0 += 32) {
     const int e = e0 + lane;
-    int begin = 0, count = 0;
+    int begin = 0, end = 0;
     if (e < p.E) {
       begin = min(max(__ldg(p.offsets + e), 0), p.R);
-      count = max(min(max(__ldg(p.offsets + e + 1), 0), p.R) - begin, 0);
+      end = min(max(__ldg(p.offsets + e + 1), 0), p.R);
     }
+    begin = max(begin, reached);
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+      const int u = __shfl_up_sync(~0u, begin, s);
+      if (lane >= s) begin = max(begin, u);
+    }
+    const int count = max(end - begin, 0);
+    reached = __shfl_sync(~0u, max(begin, end), 31);
     const int mine = tiles_of<kPair>(count) * p.p_blocks;
     int inc = mine;
 #pragma unroll

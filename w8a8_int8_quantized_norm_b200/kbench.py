@@ -9,6 +9,9 @@
     python -m w8a8_int8_quantized_norm_b200.kbench silu_mul_quant --M 16384 --K 28672
     python -m w8a8_int8_quantized_norm_b200.kbench gemm --M 4096 --N 36864 --K 9216 --rowmax
     python -m w8a8_int8_quantized_norm_b200.kbench llmint8_combine --M 16384 --N 8192 --K 8192
+    python -m w8a8_int8_quantized_norm_b200.kbench moe_route --M 16384 --experts 128 --topk 8
+    python -m w8a8_int8_quantized_norm_b200.kbench gemm_grouped --M 4096 --N 8192 --K 4096 --experts 8 --topk 2
+    python -m w8a8_int8_quantized_norm_b200.kbench block_norm --M 16384 --K 8192 --norm rms --topk 2
 
 Each call is captured once as a CUDA graph; every timed replay is bracketed by
 CUDA events on the launching stream, with L2 emptied before it (256 MiB
@@ -105,7 +108,10 @@ def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     ap.add_argument("op", choices=["norm_quant", "gemm", "calibrate", "weight_quant",
                                    "smooth_scales", "quant_given", "silu_mul_quant",
-                                   "llmint8_combine"])
+                                   "llmint8_combine", "moe_route", "gemm_grouped", "block_norm"])
+    ap.add_argument("--experts", type=int, default=8)
+    ap.add_argument("--topk", type=int, default=2,
+                    help="experts per token (block_norm: rows summed per token, 0 = none)")
     ap.add_argument("--outliers", type=int, default=8,
                     help="llmint8_combine: outlier channels of x (x50, the rest N(0, 1))")
     ap.add_argument("--M", type=int, default=4096)
@@ -161,6 +167,48 @@ def main(argv=None):
         fn = lambda: sq.silu_mul_quant_per_token(gu, xq, xs)
         units = M * 2 * K * 2 + M * K + 4 * M
         shape = {"M": M, "I": K, "dtype": "bf16"}
+    elif a.op == "moe_route":
+        logits = torch.randn((M, a.experts), generator=gen, device=dev)
+        logits = logits.to(torch.bfloat16) if a.dtype == "bf16" else logits
+        r = sq.moe_route(logits, a.topk)
+        need = sq.moe_route_workspace_size(M, a.experts, a.topk)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        fn = lambda: sq.moe_route(logits, a.topk, weights=r.weights, experts=r.experts,
+                                  offsets=r.offsets, row_token=r.row_token,
+                                  token_row=r.token_row, workspace=ws)
+        units = M * a.experts * esz + 16 * M * a.topk + 4 * (a.experts + 1)
+        shape = {"M": M, "experts": a.experts, "topk": a.topk, "dtype": a.dtype}
+    elif a.op == "gemm_grouped":
+        E, R = a.experts, M * a.topk
+        r = sq.moe_route(torch.randn((M, E), generator=gen, device=dev), a.topk)
+        A, B = _codes(M, K, gen, dev), _codes(E * N, K, gen, dev).view(E, N, K)
+        xs = torch.empty(M, device=dev).uniform_(1e-3, 1e-2, generator=gen)
+        wsc = torch.empty((E, N), device=dev).uniform_(1e-4, 1e-3, generator=gen)
+        out = torch.empty((R, N), dtype=torch.bfloat16, device=dev)
+        gemm = sq.w8a8_gemm_grouped
+        if a.fp8:
+            A, B = A.view(torch.uint8) & 0x77, B.view(torch.uint8) & 0xf7  # finite e4m3 codes
+            gemm = sq.fp8_gemm_grouped
+        fn = lambda: gemm(A, B, xs, wsc, r.offsets, row_token=r.row_token, out=out,
+                          path_hint=a.path)
+        active = int((r.offsets[1:] > r.offsets[:-1]).sum())
+        units = active * (N * K + 4 * N) + M * (K + 4) + 4 * R + 2 * R * N
+        shape = {"M": M, "N": N, "K": K, "experts": E, "topk": a.topk, "active": active,
+                 "path": a.path, "fp8": a.fp8}
+    elif a.op == "block_norm":
+        R = M * max(1, a.topk)
+        x, res = _acts(R, K, a.dtype, gen, dev), _acts(M, K, a.dtype, gen, dev)
+        rows = wts = None
+        if a.topk:
+            rows = torch.randperm(R, generator=gen, device=dev).to(torch.int32).view(M, a.topk)
+            wts = torch.rand((M, a.topk), generator=gen, device=dev)
+        g = torch.empty(K, device=dev).uniform_(0.5, 1.5, generator=gen) if norm else None
+        h, xq, xs = sq.block_norm_quant_per_token(x, res, token_row=rows, weights=wts, fp8=a.fp8)
+        fn = lambda: sq.block_norm_quant_per_token(
+            x, res, token_row=rows, weights=wts, post_norm=norm, post_gamma=g, pre_norm=norm,
+            pre_gamma=g, fp8=a.fp8, h_out=h, Xq=xq, x_scale=xs)
+        units = M * K * (esz * (max(1, a.topk) + 2) + 1) + 4 * M + (8 * K if g is not None else 0)
+        shape = {"M": M, "K": K, "norm": a.norm, "topk": a.topk, "dtype": a.dtype, "fp8": a.fp8}
     elif a.op == "llmint8_combine":
         # LLM.int8()'s merge on [M, N] outputs of a K-deep Linear: the INT32
         # accumulator read, the 16-bit lane over the outlier channels, bf16 out
@@ -237,8 +285,8 @@ def main(argv=None):
         raise SystemExit("device error: %s" % sq.status_string(err))
     line = {"op": a.op, "shape": shape, "us_per_call": us, "iters": a.iters,
             "l2": "emptied before every call, clean (untimed)", "peak_source": src}
-    if a.op == "gemm" and M > 128:
-        ops = 2.0 * M * N * K
+    if (a.op == "gemm" and M > 128) or (a.op == "gemm_grouped" and M * a.topk > 128 * a.experts):
+        ops = 2.0 * M * N * K * (a.topk if a.op == "gemm_grouped" else 1)
         line.update(achieved=ops / us / 1e6, unit="TOPS", peak=bf16 * INT8_PER_BF16,
                     algorithmic_ops=ops)
     else:
