@@ -39,6 +39,14 @@ __device__ __forceinline__ uint4 load_stream(const void* p) {
   return v;
 }
 
+__device__ __forceinline__ uint4 load_shared16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr));
+  return v;
+}
+
 // 8 consecutive values as loaded: 16 bytes of bf16 or 32 bytes of fp32.
 template <typename T>
 struct Raw8;
@@ -49,9 +57,7 @@ struct Raw8<__nv_bfloat16> {
     w = load_stream(static_cast<const __nv_bfloat16*>(p) + i);
   }
   // 16 bytes a lane: all banks once
-  __device__ __forceinline__ void load_shared(const uint8_t* buf, int c) {
-    w = *reinterpret_cast<const uint4*>(buf + c * 16);
-  }
+  __device__ __forceinline__ void load_shared(uint32_t buf, int c) { w = load_shared16(buf + c * 16); }
   __device__ __forceinline__ void get(float2 (&v)[4]) const {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -76,9 +82,9 @@ struct Raw8<float> {
     lo = load_stream(q);
     hi = load_stream(q + 4);
   }
-  __device__ __forceinline__ void load_shared(const uint8_t* buf, int c) {
-    lo = *reinterpret_cast<const uint4*>(buf + c * 32);
-    hi = *reinterpret_cast<const uint4*>(buf + c * 32 + 16);
+  __device__ __forceinline__ void load_shared(uint32_t buf, int c) {
+    lo = load_shared16(buf + c * 32);
+    hi = load_shared16(buf + c * 32 + 16);
   }
   __device__ __forceinline__ void get(float2 (&v)[4]) const {
     const uint32_t u[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
@@ -222,7 +228,7 @@ __device__ __forceinline__ uint2 codes_f8(const float2 (&v)[4], float inv) {
 
 // v (this thread's chunks) -> its norm before gamma and beta, in place.  Two
 // reductions for LayerNorm, one for RMSNorm, none without a norm.
-template <int CH>
+template <int CH, bool kFull>
 __device__ __forceinline__ void normalise(float2 (&v)[CH][4], int K, int norm, float eps,
                                           float (*slots)[32], const Team& tm) {
   if (norm == SQ_NORM_NONE) return;
@@ -238,7 +244,7 @@ __device__ __forceinline__ void normalise(float2 (&v)[CH][4], int K, int norm, f
         team_sum((s[0].x + s[0].y) + (s[1].x + s[1].y), slots[0], tm) * inv_k;
 #pragma unroll
     for (int i = 0; i < CH; ++i)
-      if (tm.thread + i * tm.threads < (K >> 3)) {  // the rest of v stays zero
+      if (kFull || tm.thread + i * tm.threads < (K >> 3)) {  // the rest of v stays zero
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[i][j] = __fadd2_rn(v[i][j], make_float2(-mu, -mu));
       }
@@ -255,14 +261,16 @@ __device__ __forceinline__ void normalise(float2 (&v)[CH][4], int K, int norm, f
   for (int i = 0; i < CH; ++i) scale8(v[i], r);
 }
 
-// The codes of y and their scale; one reduction.
-template <int CH>
+// The codes of y and their scale; one reduction.  kFull: every thread has all
+// its CH chunks (no test per chunk, so the chunks' work runs together).
+template <int CH, bool kFull>
 __device__ __forceinline__ void store_codes(const float2 (&v)[CH][4], const BlockNormParams& p,
                                             int64_t m, float* slot, const Team& tm) {
+  const int chunks = p.K >> 3;
   float am[2] = {0.0f, 0.0f};
 #pragma unroll
   for (int i = 0; i < CH; ++i)
-    if (tm.thread + i * tm.threads < (p.K >> 3)) {  // a row of NaN leaves them past its end too
+    if (kFull || tm.thread + i * tm.threads < chunks) {  // a row of NaN leaves them past its end too
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         am[0] = max_nan(am[0], fabsf(v[i][j].x));
@@ -274,13 +282,18 @@ __device__ __forceinline__ void store_codes(const float2 (&v)[CH][4], const Bloc
   if (p.fp8 && step < FLT_MIN) step = 0.0f;
   const float inv = step != 0.0f ? __fdiv_rn(1.0f, step) : 0.0f;
   if (tm.thread == 0) p.a.x_scale[m] = step;
-  uint8_t* q = static_cast<uint8_t*>(p.a.Xq) + m * p.K;
+  uint8_t* q = static_cast<uint8_t*>(p.a.Xq) + m * p.K + tm.thread * 8;
+  const int stride = tm.threads * 8;
+  if (p.fp8) {
 #pragma unroll
-  for (int i = 0; i < CH; ++i) {
-    const int c = tm.thread + i * tm.threads;
-    if (c < (p.K >> 3))
-      *reinterpret_cast<uint2*>(q + c * 8) =
-          p.fp8 ? codes_f8(v[i], inv) : codes_i8(v[i], step, inv);
+    for (int i = 0; i < CH; ++i)
+      if (kFull || tm.thread + i * tm.threads < chunks)
+        *reinterpret_cast<uint2*>(q + i * stride) = codes_f8(v[i], inv);
+  } else {
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+      if (kFull || tm.thread + i * tm.threads < chunks)
+        *reinterpret_cast<uint2*>(q + i * stride) = codes_i8(v[i], step, inv);
   }
 }
 
@@ -339,7 +352,7 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const BlockNorm
     }
   }
   const float tg = a.token_gate ? a.token_gate[m] : 1.0f;
-  normalise<CH>(v, p.K, a.post_norm, a.post_eps, slots, tm);
+  normalise<CH, false>(v, p.K, a.post_norm, a.post_eps, slots, tm);
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = tm.thread + i * tm.threads;
@@ -357,7 +370,7 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const BlockNorm
     }
   }
   if (!a.Xq) return;
-  normalise<CH>(v, p.K, a.pre_norm, a.pre_eps, slots + 2, tm);
+  normalise<CH, false>(v, p.K, a.pre_norm, a.pre_eps, slots + 2, tm);
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = tm.thread + i * tm.threads;
@@ -366,7 +379,7 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const BlockNorm
       if (a.pre_beta && a.pre_norm == SQ_NORM_LAYER) add8(v[i], GlobalVec{a.pre_beta}, c);
     }
   }
-  store_codes<CH>(v, p, m, slots[4], tm);
+  store_codes<CH, false>(v, p, m, slots[4], tm);
 }
 
 // ---------------------------------------------------------------------------
@@ -375,14 +388,21 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const BlockNorm
 // the next row's x is fetched as soon as this row's is in registers, the next
 // residual after this one, so copies are in flight through the reductions and
 // stores; with plain loads the kernel waited for them (long-scoreboard stalls
-// 8.6 of 15 warps, a third of HBM).  The parameter vectors (post_gamma * gate,
+// 8.6 of 15 warps, a third of HBM).  Bound by HBM with the rows of two experts
+// (16384 x 8192, RMSNorm twice: 192 us, 6.3 TB/s), close to it without (162 us,
+// 5.8 TB/s).  The parameter vectors (post_gamma * gate,
 // post_beta * gate, pre_gamma, pre_beta) are put into shared memory once per
 // CTA: read per row through L1 they were more bytes than the row itself.
 // ---------------------------------------------------------------------------
-constexpr int kPipeCH = 4;
 constexpr int kMaxGroups = 8;
-constexpr int kPipeMaxK = 8192;  // 256 threads a row at most
 constexpr int kPipeMaxSum = 4;   // expert rows a token sums, at most
+// Chunks of a thread and threads of a CTA.  Without a sum 64 values a thread
+// measured best (16384 x 8192: 160 us, 178 us with 32 a thread); with one the
+// rows' copies leave room for three groups at 8192 channels, and 32 values a
+// thread keep more warps (192 against 221 us).  Below 80 registers a thread the
+// same code spills and loses a third.
+__host__ __device__ constexpr int pipe_ch(bool sum) { return sum ? 4 : 8; }
+constexpr int pipe_max_threads(bool sum) { return sum ? 768 : 512; }
 
 struct PipeShape {
   int groups, threads;         // threads of a group
@@ -414,17 +434,17 @@ __device__ __forceinline__ bool mbar_try_wait_for(uint32_t bar, uint32_t parity,
 }
 
 template <typename T>
-__device__ __forceinline__ void shared8(const uint8_t* buf, int c, float2 (&v)[4]) {
+__device__ __forceinline__ void shared8(uint32_t buf, int c, float2 (&v)[4]) {
   Raw8<T> raw;
   raw.load_shared(buf, c);
   raw.get(v);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(1024, 1)
+template <typename T, bool kSum, bool kFull>
+__global__ void __launch_bounds__(pipe_max_threads(kSum), 1)
     block_norm_pipe_kernel(const BlockNormParams p, const PipeShape sh, int* error_word,
                            int64_t wait_polls) {
-  constexpr int CH = kPipeCH;
+  constexpr int CH = pipe_ch(kSum);
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float slots[kMaxGroups][5][32];
   __shared__ uint64_t bars[kMaxGroups][2];
@@ -436,9 +456,9 @@ __global__ void __launch_bounds__(1024, 1)
   const int g = static_cast<int>(threadIdx.x) / sh.threads;
   const Team tm{static_cast<int>(threadIdx.x) - g * sh.threads, sh.threads, sh.threads >> 5, 1 + g};
   float* params = reinterpret_cast<float*>(smem);
-  uint8_t* xbuf = smem + static_cast<size_t>(sh.vecs) * p.K * 4 +
-                  static_cast<size_t>(g) * (sh.x_rows + (a.residual ? 1 : 0)) * sh.row_bytes;
-  uint8_t* rbuf = xbuf + sh.x_rows * sh.row_bytes;
+  const uint32_t xbuf = smem_u32(smem) + sh.vecs * p.K * 4 +
+                        g * (sh.x_rows + (a.residual ? 1 : 0)) * sh.row_bytes;
+  const uint32_t rbuf = xbuf + sh.x_rows * sh.row_bytes;
   const uint32_t xbar = smem_u32(&bars[g][0]), rbar = smem_u32(&bars[g][1]);
   const int64_t step_rows = static_cast<int64_t>(gridDim.x) * sh.groups;
   const int64_t m0 = static_cast<int64_t>(blockIdx.x) * sh.groups + g;
@@ -460,19 +480,18 @@ __global__ void __launch_bounds__(1024, 1)
   float next_w = 0.0f;
   auto peek = [&](int64_t m) {
     next_row = -1;
-    if (a.token_row && lane < a.top_k && m < a.M) {
+    if (kSum && lane < a.top_k && m < a.M) {
       next_row = a.token_row[m * a.top_k + lane];
       next_w = a.weights[m * a.top_k + lane];
     }
   };
   auto fetch_x = [&](int64_t m, int parity) {
-    if (!a.token_row) {
+    if constexpr (!kSum) {
       if (lane == 0) {
         mbar_arrive_expect_tx(xbar, sh.row_bytes);
-        bulk_load(smem_u32(xbuf), static_cast<const T*>(a.x) + m * a.ldx, sh.row_bytes, xbar);
+        bulk_load(xbuf, static_cast<const T*>(a.x) + m * a.ldx, sh.row_bytes, xbar);
       }
-      return;
-    }
+    } else {
     const bool mine = next_row >= 0 && next_row < a.R;
     const uint32_t ok = __ballot_sync(~0u, mine);
     if (lane < a.top_k) sum_w[g][parity][lane] = next_w;
@@ -481,13 +500,14 @@ __global__ void __launch_bounds__(1024, 1)
     if (lane == 0) mbar_arrive_expect_tx(xbar, __popc(ok) * sh.row_bytes);
     __syncwarp();
     if (mine)
-      bulk_load(smem_u32(xbuf) + lane * sh.row_bytes,
+      bulk_load(xbuf + lane * sh.row_bytes,
                 static_cast<const T*>(a.x) + static_cast<int64_t>(next_row) * a.ldx, sh.row_bytes,
                 xbar);
+    }
   };
   auto fetch_res = [&](int64_t m) {
     mbar_arrive_expect_tx(rbar, sh.row_bytes);
-    bulk_load(smem_u32(rbuf), static_cast<const T*>(a.residual) + m * a.ld_res, sh.row_bytes, rbar);
+    bulk_load(rbuf, static_cast<const T*>(a.residual) + m * a.ld_res, sh.row_bytes, rbar);
   };
   if (fetcher && m0 < a.M) {
     peek(m0);
@@ -526,64 +546,92 @@ __global__ void __launch_bounds__(1024, 1)
     const bool more = m + step_rows < a.M;
     float2 v[CH][4];
     const float tg = a.token_gate ? __ldg(a.token_gate + m) : 1.0f;
+    // one loop over the chunks per step, its condition outside: the chunks'
+    // loads then go out together
+    auto in = [&](int i) { return kFull || tm.thread + i * tm.threads < chunks; };
+    auto at = [&](int i) { return tm.thread + i * tm.threads; };
     wait(xbar);
+    // (a test at run time, although kSum says the same: without it the loads are
+    // all moved up and spill, 200 us instead of 162 at 16384 x 8192)
+    if (!a.token_row) {
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[i][j] = make_float2(0.0f, 0.0f);
-      const int c = tm.thread + i * tm.threads;
-      if (c < chunks) {
-        if (!a.token_row) {
-          shared8<T>(xbuf, c, v[i]);
+      for (int i = 0; i < CH; ++i) {
+        if (in(i)) {
+          shared8<T>(xbuf, at(i), v[i]);
         } else {
-          const int ok = sum_ok[g][phase];
-          for (int k = 0; k < a.top_k; ++k) {
-            if ((ok >> k) & 1) {
-              const float w = sum_w[g][phase][k];
-              float2 t[4];
-              shared8<T>(xbuf + k * sh.row_bytes, c, t);
-              fma8(v[i], w, t);
-            }
-          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[i][j] = make_float2(0.0f, 0.0f);
         }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < CH; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[i][j] = make_float2(0.0f, 0.0f);
+      const int ok = sum_ok[g][phase];
+      for (int k = 0; k < a.top_k; ++k) {
+        if (!((ok >> k) & 1)) continue;
+        const float w = sum_w[g][phase][k];
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
+          if (in(i)) {
+            float2 t[4];
+            shared8<T>(xbuf + k * sh.row_bytes, at(i), t);
+            fma8(v[i], w, t);
+          }
       }
     }
     if (a.post_norm == SQ_NORM_NONE) tm.sync();  // the row is in registers (else: by the sum)
-    normalise<CH>(v, p.K, a.post_norm, a.post_eps, slots[g], tm);
+    normalise<CH, kFull>(v, p.K, a.post_norm, a.post_eps, slots[g], tm);
     if (fetcher && more) {
       fetch_x(m + step_rows, phase ^ 1u);
       peek(m + 2 * step_rows);
     }
-    if (a.residual) wait(rbar);
+    if (vec[0]) {
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int c = tm.thread + i * tm.threads;
-      if (c < chunks) {
-        if (vec[0]) mul8(v[i], vec[0], c);
-        if (vec[1]) add8(v[i], vec[1], c);
-        if (a.token_gate) scale8(v[i], tg);
-        if (a.residual) {
+      for (int i = 0; i < CH; ++i)
+        if (in(i)) mul8(v[i], vec[0], at(i));
+    }
+    if (vec[1]) {
+#pragma unroll
+      for (int i = 0; i < CH; ++i)
+        if (in(i)) add8(v[i], vec[1], at(i));
+    }
+    if (a.token_gate) {
+#pragma unroll
+      for (int i = 0; i < CH; ++i) scale8(v[i], tg);
+    }
+    if (a.residual) {
+      wait(rbar);
+#pragma unroll
+      for (int i = 0; i < CH; ++i)
+        if (in(i)) {
           float2 t[4];
-          shared8<T>(rbuf, c, t);
+          shared8<T>(rbuf, at(i), t);
           fma8(v[i], a.residual_scale, t);
         }
-        if (a.h_out) Raw8<T>::store(a.h_out, m * a.ld_h + c * 8, v[i]);
-      }
+    }
+    if (a.h_out) {
+#pragma unroll
+      for (int i = 0; i < CH; ++i)
+        if (in(i)) Raw8<T>::store(a.h_out, m * a.ld_h + at(i) * 8, v[i]);
     }
     if (a.Xq) {
-      normalise<CH>(v, p.K, a.pre_norm, a.pre_eps, slots[g] + 2, tm);
+      normalise<CH, kFull>(v, p.K, a.pre_norm, a.pre_eps, slots[g] + 2, tm);
       // (a sum's barrier, or the maximum's below, follows the residual's reads)
       const bool early = a.pre_norm != SQ_NORM_NONE;
       if (a.residual && early && tm.thread == 0 && more) fetch_res(m + step_rows);
+      if (vec[2]) {
 #pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        const int c = tm.thread + i * tm.threads;
-        if (c < chunks) {
-          if (vec[2]) mul8(v[i], vec[2], c);
-          if (vec[3]) add8(v[i], vec[3], c);
-        }
+        for (int i = 0; i < CH; ++i)
+          if (in(i)) mul8(v[i], vec[2], at(i));
       }
-      store_codes<CH>(v, p, m, slots[g][4], tm);
+      if (vec[3]) {
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
+          if (in(i)) add8(v[i], vec[3], at(i));
+      }
+      store_codes<CH, kFull>(v, p, m, slots[g][4], tm);
       if (a.residual && !early && tm.thread == 0 && more) fetch_res(m + step_rows);
     } else {
       tm.sync();
@@ -600,28 +648,40 @@ __global__ void __launch_bounds__(1024, 1)
 
 // Groups of the pipeline for these arguments, or false if it does not pay:
 // fewer than two groups fit (their copies would not overlap a row's
-// reductions), or there are too few rows to fill it twice (measured on 148
-// SMs, 4096 channels: see the launch below).
+// reductions), or there are too few rows for every group to have two.
 bool pipe_shape(const sq_block_norm_args& a, int sms, PipeShape& sh) {
   const int K = static_cast<int>(a.K), es = a.dtype == SQ_BF16 ? 2 : 4;
-  if (K > kPipeMaxK || a.top_k > kPipeMaxSum) return false;
-  sh.vecs = 0;
+  const bool sum = a.token_row != nullptr;
+  if (a.top_k > kPipeMaxSum) return false;
+  sh.threads = ((K / 8 + pipe_ch(sum) - 1) / pipe_ch(sum) + 31) / 32 * 32;
+  sh.x_rows = sum ? a.top_k : 1;
+  sh.row_bytes = K * es;
+  const int group = (sh.x_rows + (a.residual ? 1 : 0)) * sh.row_bytes;
   const bool has[4] = {a.post_gamma || a.gate, a.post_beta && a.post_norm == SQ_NORM_LAYER,
                        a.Xq && a.pre_gamma,
                        a.Xq && a.pre_beta && a.pre_norm == SQ_NORM_LAYER};
+  sh.vecs = 0;
   for (int i = 0; i < 4; ++i) sh.vec_at[i] = has[i] ? sh.vecs++ : -1;
-  sh.threads = ((K / 8 + kPipeCH - 1) / kPipeCH + 31) / 32 * 32;
-  sh.x_rows = a.top_k > 0 ? a.top_k : 1;
-  sh.row_bytes = K * es;
-  const int group = (sh.x_rows + (a.residual ? 1 : 0)) * sh.row_bytes;
-  const int room = 220 * 1024 - sh.vecs * K * 4;
-  int n = room / group;
-  if (n > 1024 / sh.threads) n = 1024 / sh.threads;
+  int n = (221 * 1024 - sh.vecs * K * 4) / group;
+  if (n > pipe_max_threads(sum) / sh.threads) n = pipe_max_threads(sum) / sh.threads;
   if (n > kMaxGroups) n = kMaxGroups;
   if (n < 2 || a.M < static_cast<int64_t>(2) * n * sms) return false;
   sh.groups = n;
   sh.smem = sh.vecs * K * 4 + n * group;
   return true;
+}
+
+template <typename T, bool kSum>
+cudaError_t launch_pipe(const BlockNormParams& p, const PipeShape& sh, int sms, int* error_word,
+                        int64_t wait_polls, cudaLaunchConfig_t cfg) {
+  auto kern = (p.K >> 3) == pipe_ch(kSum) * sh.threads ? block_norm_pipe_kernel<T, kSum, true>
+                                                       : block_norm_pipe_kernel<T, kSum, false>;
+  cudaError_t e = launch_cache().ensure_smem(reinterpret_cast<const void*>(kern), sh.smem);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(static_cast<unsigned>(sms));
+  cfg.blockDim = dim3(static_cast<unsigned>(sh.groups * sh.threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(sh.smem);
+  return cudaLaunchKernelEx(&cfg, kern, p, sh, error_word, wait_polls);
 }
 
 template <typename T>
@@ -636,15 +696,9 @@ cudaError_t launch_block_norm_t(const BlockNormParams& p, int sms, int64_t wait_
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   PipeShape sh;
-  if (pipe_shape(p.a, sms, sh)) {
-    auto kern = block_norm_pipe_kernel<T>;
-    cudaError_t e = launch_cache().ensure_smem(reinterpret_cast<const void*>(kern), sh.smem);
-    if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(static_cast<unsigned>(sms));
-    cfg.blockDim = dim3(static_cast<unsigned>(sh.groups * sh.threads));
-    cfg.dynamicSmemBytes = static_cast<size_t>(sh.smem);
-    return cudaLaunchKernelEx(&cfg, kern, p, sh, error_word, wait_polls);
-  }
+  if (pipe_shape(p.a, sms, sh))
+    return p.a.token_row ? launch_pipe<T, true>(p, sh, sms, error_word, wait_polls, cfg)
+                         : launch_pipe<T, false>(p, sh, sms, error_word, wait_polls, cfg);
   cfg.gridDim = dim3(static_cast<unsigned>(p.a.M));
   auto threads = [&](int ch) { return static_cast<unsigned>(((chunks + ch - 1) / ch + 31) / 32 * 32); };
   if (chunks <= 1024) {
