@@ -686,3 +686,62 @@ def test_binding_refusals():
                                       weights=torch.zeros((4, 1), device="cuda"))
     with pytest.raises(sq.SQError):
         sq.block_norm_quant_per_token(torch.zeros((4, 72), device="cuda"))  # K % 16
+
+
+# ---------------------------------------------------------------------------
+# addresses past 32 bits
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("path", [1, 2])
+def test_grouped_output_past_32_bits(path):
+    """R N > 2^31 outputs: the last rows are right, and so are the first."""
+    R, N, K = 70000, 32768, 16
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(5)
+    x = torch.randint(-127, 128, (R, K), generator=gen, device="cuda", dtype=torch.int8)
+    w = torch.randint(-127, 128, (2, N, K), generator=gen, device="cuda", dtype=torch.int8)
+    off = _cuda_of(np.array([0, 100, R], np.int32))
+    one = torch.ones(R, device="cuda")
+    out = sq.w8a8_gemm_grouped(x, w, one, torch.ones((2, N), device="cuda"), off, path_hint=path)
+    for rows, e in ((slice(0, 50), 0), (slice(R // 2, R // 2 + 50), 1), (slice(R - 50, R), 1)):
+        want = (x[rows].double() @ w[e].double().T).float().to(torch.bfloat16)
+        assert torch.equal(out[rows], want)
+
+
+@pytest.mark.parametrize("path", [1, 2])
+def test_grouped_weights_past_32_bits(path):
+    E, N, K = 70, 8192, 4096
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(6)
+    w = torch.randint(-127, 128, (E, N, K), generator=gen, device="cuda", dtype=torch.int8)
+    x = torch.randint(-127, 128, (40, K), generator=gen, device="cuda", dtype=torch.int8)
+    off = np.zeros(E + 1, np.int32)
+    off[36:] = 10
+    off[E:] = 40  # rows for experts 35 and 69
+    out = sq.w8a8_gemm_grouped(x, w, None, None, _cuda_of(off), epi="i32", path_hint=path)
+    for rows, e in ((slice(0, 10), 35), (slice(10, 40), 69)):
+        assert torch.equal(out[rows].double(), x[rows].double() @ w[e].double().T)
+
+
+@pytest.mark.parametrize("top_k", [0, 2])
+def test_block_norm_past_32_bits(top_k):
+    """M K > 2^31 values: sampled rows equal the same rows in a batch of their own
+    (as far as the sums' order allows)."""
+    M, K = 264000, 8192
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(7)
+    x = torch.empty((M, K), dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    pick = torch.tensor([0, 1, M // 2, M - 2, M - 1], device="cuda")
+    rows = w = None
+    if top_k:
+        rows = torch.randint(0, M, (M, 2), device="cuda", dtype=torch.int32, generator=gen)
+        w = torch.rand((M, 2), device="cuda", generator=gen)
+    h, q, s = sq.block_norm_quant_per_token(x, x, token_row=rows, weights=w, post_norm=sq.NORM_RMS)
+    x64, r64 = _np64(x[pick]), _np64(x[pick])
+    if top_k:
+        x64 = sum(_np64(x[rows[pick][:, j].long()]) * _np64(w[pick])[:, j:j + 1] for j in range(2))
+    hr, dh, y, dy = ref.block_norm(x64, r64, None, None, ("rms", None, None, 1e-5), None, None, 1.0,
+                                   ("rms", None, None, 1e-5))
+    dh, dy = dh * 1.1 + 4 * ref.U * np.abs(hr).max(), dy * 1.1 + 8 * ref.U * np.abs(y).max()  # the sum of two rows
+    assert (np.abs(_np64(h[pick]) - hr) <= dh + 2.0 ** -8 * (np.abs(hr) + dh)).all()
+    ref.check_codes(_np64(q[pick].float()), _np64(s[pick]), y, dy, 127.0)

