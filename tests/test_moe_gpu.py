@@ -228,6 +228,27 @@ def test_grouped_epilogues(epi, fp8, path):
     _check_grouped([5, 0, 300, 2], 150, 528, fp8, path=path, epi=epi)
 
 
+@pytest.mark.parametrize("fp8", [False, True], ids=["int8", "fp8"])
+@pytest.mark.parametrize("N,pad", [(7, 1), (129, 7), (250, 6), (257, 7), (1003, 5), (128, 4), (300, 1)])
+def test_grouped_output_rows_of_any_stride(N, pad, fp8):
+    """16-byte rows whose last columns do not fill 16 bytes, and rows that are not 16-byte."""
+    _check_grouped([5, 0, 300, 2], N, 272, fp8, gather=33, path=1, pad=pad)
+    _check_grouped([5, 0, 40, 2], N, 272, fp8, path=2, pad=pad, epi="bf16_relu")
+
+
+@pytest.mark.parametrize("path", [1, 2])
+def test_grouped_output_at_an_odd_address(path):
+    rng = _rng(15)
+    xq, wq = _cuda_of(_codes(rng, (300, 160), False)), _cuda_of(_codes(rng, (2, 96, 160), False))
+    xs, ws = torch.rand(300, device="cuda"), torch.rand((2, 96), device="cuda")
+    off = _cuda_of(np.array([0, 290, 300], np.int32))
+    want = sq.w8a8_gemm_grouped(xq, wq, xs, ws, off, path_hint=path)
+    buf = torch.full((300, 104), 9.0, dtype=torch.bfloat16, device="cuda")
+    sq.w8a8_gemm_grouped(xq, wq, xs, ws, off, out=buf[:, 1:97], path_hint=path)
+    assert torch.equal(buf[:, 1:97], want)
+    assert (buf[:, 0] == 9).all() and (buf[:, 97:] == 9).all()
+
+
 @pytest.mark.parametrize("path", [0, 1, 2])
 def test_grouped_rows_before_the_first_group(path):
     _check_grouped([6, 40], 64, 64, path=path, first=9, extra_rows=4)
@@ -373,6 +394,45 @@ def test_block_norm_many_rows():
     _check_block(3000, 2048)
     _check_block(2500, 4096, top_k=2, post="none", token_gate=True)
     _check_block(700, 8192, post="layer", pre="layer", dtype=torch.float32)
+
+
+@pytest.mark.parametrize("K", [16, 272, 1024, 1040])
+@pytest.mark.parametrize("post", ["none", "rms", "layer"])
+@pytest.mark.parametrize("pre", ["none", "rms", "layer"])
+@pytest.mark.parametrize("top_k", [0, 1, 4, 5])
+def test_block_norm_pipeline_forms(top_k, pre, post, K):
+    """Enough rows that every group of the pipeline runs several (five summed rows: without it)."""
+    M = 5200 if K < 1024 else 2600
+
+    def tweak(v):
+        if top_k:
+            v["tr"][::7, 0] = -1
+            v["tr"][3] = -1
+
+    for residual, gate, tg, params in ((True, True, False, True), (False, False, True, False)):
+        _check_block(M, K, post=post, pre=pre, top_k=top_k, R=700 if top_k else None, gate=gate,
+                     token_gate=tg, residual=residual, params=params, fp8=K == 272, tweak=tweak,
+                     dtype=torch.float32 if K == 16 else torch.bfloat16, pad=8)
+
+
+@pytest.mark.parametrize("post", ["none", "rms"])
+@pytest.mark.parametrize("residual", [True, False])
+def test_block_norm_pipeline_without_codes(post, residual):
+    x, res = torch.randn((6000, 512), device="cuda"), torch.randn((6000, 512), device="cuda")
+    h, q, s = sq.block_norm_quant_per_token(x, res if residual else None, post_norm=NORM[post], quant=False)
+    assert q is None and s is None
+    want, *_ = sq.block_norm_quant_per_token(x, res if residual else None, post_norm=NORM[post])
+    assert torch.equal(h, want)
+    if post == "none":
+        assert torch.equal(h, x + res if residual else x)
+
+
+@pytest.mark.parametrize("alias", ["residual", "x"])
+def test_block_norm_in_place_pipelined(alias):
+    a = _check_block(5000, 512, alias=alias, pad=16, seed=4)
+    b = _check_block(5000, 512, pad=16, seed=4)
+    for u, v in zip(a, b):
+        assert torch.equal(u, v)
 
 
 @pytest.mark.parametrize("alias", ["residual", "x"])
