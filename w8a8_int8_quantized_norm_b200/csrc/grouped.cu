@@ -23,8 +23,8 @@
 // spread unevenly; one token's two experts 15 us (67 MB, 0.65 of HBM).  Bound by
 // the MMA and the delivery of its operands, decode tiles by the weight stream.
 // Warp roles as in gemm.cu: 0 producer, 1 MMA issuer, 2-5 epilogue, 6 the
-// issuer's scheduler; 7-10 gather tokens.  Every wait is bounded; one that runs out records
-// SQ_ERR_PIPELINE_TIMEOUT and the CTAs drain and return.
+// issuer's scheduler; 7-10 gather tokens.  Every wait is bounded; one that runs
+// out records SQ_ERR_PIPELINE_TIMEOUT and the CTAs drain and return.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -754,7 +754,9 @@ cudaError_t launch_gemm_grouped(const void* Xq, int64_t X, const void* Wq, const
   const int sms = num_sms > 0 ? num_sms : 148;
   // decode tiles while an expert has few rows: they keep more weight blocks in
   // flight and need no cluster; past 32 rows an expert's weights would be read
-  // again for every 32
+  // again for every 32.  Measured, decode / pair: 2 rows of 2 experts 2048 x 1024
+  // 10.8 / 13.9 us, 24 rows of each of 64 experts 2048 x 4096 90.9 / 94.6 us, 100
+  // rows of each of 16 experts 4000 x 1040 43.9 / 32.7 us, 4096 x 4096 104 / 62 us
   const bool pair = path_hint == 1 || (path_hint == 0 && R > 24 * E);
   GroupedParams p{};
   p.x_scale = x_scale;

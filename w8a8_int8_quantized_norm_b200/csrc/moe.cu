@@ -9,9 +9,10 @@
 // tokens at once, so that one's maxima are in flight behind the other's, and
 // sorts each lane's keys first, so that a choice looks at one of them.  A CTA
 // walks a contiguous range of tokens in groups of 64; within a group each expert
-// keeps a 64-bit mask of the tokens that chose it (a token chooses an expert at most once), so a
-// row's rank among the group's rows of that expert is a population count --
-// stable in token order whatever order the mask's atomics arrived in.  The
+// keeps a 64-bit mask of the tokens that chose it (a token chooses an expert at
+// most once), so a row's rank among the group's rows of that expert is a
+// population count -- stable in token order whatever order the mask's atomics
+// arrived in.  The
 // second pass adds, per expert, the counts of all earlier CTAs and experts and
 // scatters.  With one CTA's worth of tokens the first pass scatters itself.
 // Bound by instructions, not by its 6 MB: 16384 tokens, 128 experts, top 8 take
@@ -83,8 +84,11 @@ __device__ __forceinline__ float load_logit(const __nv_bfloat16* p) { return __b
 __device__ __forceinline__ float load_logit(const float* p) { return *p; }
 
 // The choices of U tokens by one warp: lane j < top_k gets each token's j-th
-// expert (-1: none left, or no token) and its weight.  V: experts per lane.  Key 0 marks an
-// expert that cannot be chosen (every finite value's key is above it).
+// expert (-1: none left, or no token) and its weight.  V: experts per lane.
+// Key 0 marks an expert that cannot be chosen (every finite value's key is above
+// it).  Up to 4 keys a lane are sorted first: 6 exchanges, then a choice costs
+// one maximum and a shift (16384 x 128, top 8: 28.6 us against 34.8 searching);
+// 8 and 16 keys would need 28 and 120 exchanges, and are searched.
 template <typename T, int V, int U, bool kBias>
 __device__ __forceinline__ void choose(const RouteParams& p, const int64_t (&t)[U], int64_t t_end,
                                        int lane, int (&my_e)[U], float (&my_w)[U]) {
