@@ -807,9 +807,11 @@ const char* sq_status_string(sq_status status);
 sq_status sq_get_device_error(void* stream);
 
 /*
- * sq_set_wait_limit -- diagnostics: the number of polls after which a GEMM
- * pipeline wait gives up, records SQ_ERR_PIPELINE_TIMEOUT and lets the kernel
- * drain and return (default 0 = the built-in limit of about two seconds of SM clock).
+ * sq_set_wait_limit -- diagnostics: the number of polls after which a pipeline
+ * wait of a GEMM or of sq_block_norm_quant_per_token gives up, records
+ * SQ_ERR_PIPELINE_TIMEOUT and lets the kernel drain and return (default 0 = the
+ * built-in limit of about two seconds of SM clock).  What such a call wrote is
+ * not to be used.
  * Affects launches made after the call, from any thread.
  */
 void sq_set_wait_limit(int64_t polls);

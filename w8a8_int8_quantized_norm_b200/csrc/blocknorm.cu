@@ -433,6 +433,19 @@ __device__ __forceinline__ bool mbar_try_wait_for(uint32_t bar, uint32_t parity,
   return ok != 0;
 }
 
+// One probe that does not suspend the thread.
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 template <typename T>
 __device__ __forceinline__ void shared8(uint32_t buf, int c, float2 (&v)[4]) {
   Raw8<T> raw;
@@ -450,6 +463,7 @@ __global__ void __launch_bounds__(pipe_max_threads(kSum), 1)
   __shared__ uint64_t bars[kMaxGroups][2];
   __shared__ float sum_w[kMaxGroups][2][kPipeMaxSum];  // weights of the row being fetched, by parity
   __shared__ int sum_ok[kMaxGroups][2];                // which of its rows exist, a bit each
+  __shared__ int late[kMaxGroups][2];                  // a wait of the row ran out, by parity
   __shared__ int abort_flag;
   const sq_block_norm_args& a = p.a;
   const int chunks = p.K >> 3;
@@ -465,6 +479,7 @@ __global__ void __launch_bounds__(pipe_max_threads(kSum), 1)
 
   if (threadIdx.x == 0) abort_flag = 0;
   if (tm.thread == 0) {
+    late[g][0] = late[g][1] = 0;
     mbar_init(xbar, 1);
     mbar_init(rbar, 1);
     mbar_fence_init();
@@ -533,15 +548,28 @@ __global__ void __launch_bounds__(pipe_max_threads(kSum), 1)
 
   uint32_t phase = 0;
   // The first probe sleeps up to 20 us in hardware: a group that spins takes
-  // issue slots from the ones at work.  A wait that runs out is recorded; the
-  // rows still go through (their barriers must be met), without waiting any more.
+  // issue slots from the ones at work.  A wait that runs out is recorded and
+  // marks its row late.  The row goes through (the others wait at its barriers),
+  // but a barrier whose phase the arming thread gave up on may still be open: it
+  // is armed no more and no copy follows, and behind the row the group leaves.
+  // The marks are read behind the row's last barrier, and by parity, since a
+  // thread may be a row ahead of one that still reads.  (16384 x 8192 behind two
+  // experts: 187 us; 191 with a flag in a register joined at that barrier, 191
+  // with the marks read before every copy.)  A limit of n polls allows n - 1
+  // probes, which do not sleep: 1 always runs out.
   auto wait = [&](uint32_t bar) {
-    if (wait_polls <= 0 && mbar_try_wait_for(bar, phase, 20000u)) return;
-    if (!wait_phase(bar, phase, wait_polls, &abort_flag)) {
-      record_device_error(error_word, SQ_ERR_PIPELINE_TIMEOUT);
-      *const_cast<volatile int*>(&abort_flag) = 1;
+    if (wait_polls > 0) {
+      for (int64_t i = 1; i < wait_polls; ++i)
+        if (mbar_test_wait(bar, phase)) return true;
+    } else if (mbar_try_wait_for(bar, phase, 20000u) || wait_phase(bar, phase, 0, &abort_flag)) {
+      return true;
     }
+    record_device_error(error_word, SQ_ERR_PIPELINE_TIMEOUT);
+    *const_cast<volatile int*>(&late[g][phase]) = 1;
+    *const_cast<volatile int*>(&abort_flag) = 1;
+    return false;
   };
+  auto on_time = [&]() { return *const_cast<volatile int*>(&late[g][phase]) == 0; };
   for (int64_t m = m0; m < a.M; m += step_rows, phase ^= 1u) {
     const bool more = m + step_rows < a.M;
     float2 v[CH][4];
@@ -550,7 +578,8 @@ __global__ void __launch_bounds__(pipe_max_threads(kSum), 1)
     // loads then go out together
     auto in = [&](int i) { return kFull || tm.thread + i * tm.threads < chunks; };
     auto at = [&](int i) { return tm.thread + i * tm.threads; };
-    wait(xbar);
+    bool r_ok = true;
+    const bool x_ok = wait(xbar);
     // (a test at run time, although kSum says the same: without it the loads are
     // all moved up and spill, 200 us instead of 162 at 16384 x 8192)
     if (!a.token_row) {
@@ -583,7 +612,7 @@ __global__ void __launch_bounds__(pipe_max_threads(kSum), 1)
     }
     if (a.post_norm == SQ_NORM_NONE) tm.sync();  // the row is in registers (else: by the sum)
     normalise<CH, kFull>(v, p.K, a.post_norm, a.post_eps, slots[g], tm);
-    if (fetcher && more) {
+    if (fetcher && more && __all_sync(~0u, x_ok)) {
       fetch_x(m + step_rows, phase ^ 1u);
       peek(m + 2 * step_rows);
     }
@@ -602,7 +631,7 @@ __global__ void __launch_bounds__(pipe_max_threads(kSum), 1)
       for (int i = 0; i < CH; ++i) scale8(v[i], tg);
     }
     if (a.residual) {
-      wait(rbar);
+      r_ok = wait(rbar);
 #pragma unroll
       for (int i = 0; i < CH; ++i)
         if (in(i)) {
@@ -620,7 +649,7 @@ __global__ void __launch_bounds__(pipe_max_threads(kSum), 1)
       normalise<CH, kFull>(v, p.K, a.pre_norm, a.pre_eps, slots[g] + 2, tm);
       // (a sum's barrier, or the maximum's below, follows the residual's reads)
       const bool early = a.pre_norm != SQ_NORM_NONE;
-      if (a.residual && early && tm.thread == 0 && more) fetch_res(m + step_rows);
+      if (a.residual && early && tm.thread == 0 && more && r_ok) fetch_res(m + step_rows);
       if (vec[2]) {
 #pragma unroll
         for (int i = 0; i < CH; ++i)
@@ -632,11 +661,12 @@ __global__ void __launch_bounds__(pipe_max_threads(kSum), 1)
           if (in(i)) add8(v[i], vec[3], at(i));
       }
       store_codes<CH, kFull>(v, p, m, slots[g][4], tm);
-      if (a.residual && !early && tm.thread == 0 && more) fetch_res(m + step_rows);
+      if (a.residual && !early && tm.thread == 0 && more && r_ok) fetch_res(m + step_rows);
     } else {
       tm.sync();
-      if (a.residual && tm.thread == 0 && more) fetch_res(m + step_rows);
+      if (a.residual && tm.thread == 0 && more && r_ok) fetch_res(m + step_rows);
     }
+    if (!on_time()) break;
   }
   if (*const_cast<volatile int*>(&abort_flag)) {
     // about 20 ms: every copy in flight lands before the shared memory goes
