@@ -70,3 +70,158 @@ def test_block_norm_wait_limit(top_k, pre, quant, limit):
     assert sq.get_device_error() == 0
     for a, b in zip(got, want):
         assert (a is None and b is None) or torch.equal(a, b)
+
+
+# ---------------------------------------------------------------------------
+# memory of the stream that the work runs on
+# ---------------------------------------------------------------------------
+
+class _Allocations:
+    """Records the current stream of every torch.empty / torch.zeros on the GPU."""
+
+    def __init__(self, monkeypatch):
+        self.streams = []
+        for name in ("empty", "zeros"):
+            monkeypatch.setattr(torch, name, self._recording(getattr(torch, name)))
+
+    def _recording(self, make):
+        def call(*args, **kw):
+            self.streams.append(torch.cuda.current_stream())
+            return make(*args, **kw)
+        return call
+
+
+def _binding_calls():
+    """Every call of the binding that allocates, as a function of the stream alone."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(3)
+    M, N, K = 40, 96, 256
+    rand = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    x, W = rand(M, K).to(torch.bfloat16), rand(N, K).to(torch.bfloat16)
+    gu = rand(M, 2 * K).to(torch.bfloat16)
+    vec, amax = rand(K).abs() + 0.5, rand(M).abs() + 5
+    xq = torch.randint(-127, 128, (M, K), generator=gen, device="cuda", dtype=torch.int8)
+    wq = torch.randint(-127, 128, (N, K), generator=gen, device="cuda", dtype=torch.int8)
+    x8, w8 = xq.view(torch.uint8) & 0x77, wq.view(torch.uint8) & 0x77
+    xs, ws = rand(M).abs(), rand(N).abs()
+    acc = torch.randint(-1000, 1000, (M, N), generator=gen, device="cuda", dtype=torch.int32)
+    idx = torch.arange(K, device="cuda", dtype=torch.int32)
+    count = torch.full((1,), 3, device="cuda", dtype=torch.int32)
+    one = vec.abs().max().reshape(1)
+    logits = rand(M, 8)
+    off = _cuda_of(np.array([0, 10, M], np.int32))
+    we, wse = wq.view(2, N // 2, K), ws.view(2, N // 2)
+    rms = sq.NORM_RMS
+    # long in K, so that the decode GEMM splits and takes a workspace
+    xl, wl = xq.repeat(1, 64)[:16].contiguous(), wq.repeat(1, 64)
+    return {
+        "calibrate_absmax": lambda s: sq.calibrate_absmax(x, rms, vec, stream=s),
+        "compute_smooth_scales": lambda s: sq.compute_smooth_scales(vec, [W], 0.5, gamma=vec, beta=vec, stream=s),
+        "weight_column_max": lambda s: sq.weight_column_max([W], stream=s),
+        "smooth_scales_from_maxima": lambda s: sq.smooth_scales_from_maxima(vec, vec, 0.5, gamma=vec, beta=vec,
+                                                                            stream=s),
+        "smooth_quantize_weights": lambda s: sq.smooth_quantize_weights(W, vec, stream=s),
+        "smooth_quantize_weights_fp8": lambda s: sq.smooth_quantize_weights_fp8(W, vec, stream=s),
+        "smooth_quantize_weights_per_tensor": lambda s: sq.smooth_quantize_weights_per_tensor(W, vec, stream=s),
+        "norm_smooth_quant_per_token": lambda s: sq.norm_smooth_quant_per_token(x, rms, vec, stream=s),
+        "norm_smooth_quant_per_token_fp8": lambda s: sq.norm_smooth_quant_per_token_fp8(x, rms, vec, stream=s),
+        "norm_smooth_absmax": lambda s: sq.norm_smooth_absmax(x, rms, vec, stream=s),
+        "norm_smooth_quant_per_tensor": lambda s: sq.norm_smooth_quant_per_tensor(x, rms, one, vec, stream=s),
+        "quant_per_token_given_absmax": lambda s: sq.quant_per_token_given_absmax(x, amax, stream=s),
+        "row_absmax": lambda s: sq.row_absmax(x, stream=s),
+        "dequant_i32": lambda s: sq.dequant_i32(acc, xs, ws, stream=s),
+        "llmint8_outliers": lambda s: sq.llmint8_outliers(vec, 1.0, stream=s)[::2],
+        "llmint8_combine": lambda s: sq.llmint8_combine(acc, xs, ws, x, W, idx, count, stream=s),
+        "silu_mul_quant_per_token": lambda s: sq.silu_mul_quant_per_token(gu, stream=s),
+        "silu_mul_quant_per_token_fp8": lambda s: sq.silu_mul_quant_per_token(gu, stream=s, fp8=True),
+        "fp8_gemm_dequant": lambda s: sq.fp8_gemm_dequant(x8, w8, xs, ws, stream=s),
+        "w8a8_gemm_dequant": lambda s: sq.w8a8_gemm_dequant(xq, wq, xs, ws, stream=s),
+        "w8a8_gemm_dequant_split": lambda s: sq.w8a8_gemm_dequant(xl, wl, None, None, "i32", path_hint=2,
+                                                                  split_k=4, stream=s),
+        "w8a8_gemm_dequant_rowmax": lambda s: sq.w8a8_gemm_dequant_rowmax(xq, wq, xs, ws, path_hint=1, stream=s),
+        "linear_w8a8": lambda s: sq.linear_w8a8(x, rms, vec, None, 1e-5, wq, ws, stream=s),
+        "moe_route": lambda s: sq.moe_route(logits, 2, stream=s),
+        "w8a8_gemm_grouped": lambda s: sq.w8a8_gemm_grouped(xq, we, xs, wse, off, stream=s),
+        "fp8_gemm_grouped": lambda s: sq.fp8_gemm_grouped(x8, w8.view(2, N // 2, K), xs, wse, off, stream=s),
+        "block_norm_quant_per_token": lambda s: sq.block_norm_quant_per_token(x, x, stream=s),
+    }
+
+
+def _tensors(got):
+    return [got] if torch.is_tensor(got) else [t for t in got if t is not None]
+
+
+CALLS = ["calibrate_absmax", "compute_smooth_scales", "weight_column_max", "smooth_scales_from_maxima",
+         "smooth_quantize_weights", "smooth_quantize_weights_fp8", "smooth_quantize_weights_per_tensor",
+         "norm_smooth_quant_per_token", "norm_smooth_quant_per_token_fp8", "norm_smooth_absmax",
+         "norm_smooth_quant_per_tensor", "quant_per_token_given_absmax", "row_absmax", "dequant_i32",
+         "llmint8_outliers", "llmint8_combine", "silu_mul_quant_per_token", "silu_mul_quant_per_token_fp8",
+         "fp8_gemm_dequant", "w8a8_gemm_dequant", "w8a8_gemm_dequant_split", "w8a8_gemm_dequant_rowmax",
+         "linear_w8a8", "moe_route", "w8a8_gemm_grouped", "fp8_gemm_grouped", "block_norm_quant_per_token"]
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_outputs_and_scratch_come_from_the_stream_of_the_call(name, monkeypatch):
+    """A block of the caller's stream's memory may still be in use there, and nothing orders that
+    stream against the call's: what a call allocates is the memory of the stream it runs on."""
+    call = _binding_calls()[name]
+    want = [t.clone() for t in _tensors(call(None))]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    seen = _Allocations(monkeypatch)
+    got = _tensors(call(side))
+    side.synchronize()
+    assert seen.streams and all(s == side for s in seen.streams)
+    assert torch.cuda.current_stream() != side
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+def _layer(fmt, T=70, E=8, H=256, I=160, top_k=2, **kw):
+    from w8a8_int8_quantized_norm_b200 import moe
+
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(11)
+    rand = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    gu, dn = (rand(E, 2 * I, H) * 0.05).to(torch.bfloat16), (rand(E, H, I) * 0.05).to(torch.bfloat16)
+    x, res, gamma = rand(T, H).to(torch.bfloat16), rand(T, H).to(torch.bfloat16), rand(H).abs() + 0.5
+    layer = moe.MoELayer(gu, dn, top_k, fmt=fmt, **kw)
+    act = sq.calibrate_absmax(x, sq.NORM_RMS, gamma)
+    layer.prepare(act, 0.5, gamma)
+    norm = sq.norm_smooth_quant_per_token if fmt == "int8" else sq.norm_smooth_quant_per_token_fp8
+    Xq, xs = norm(x, sq.NORM_RMS, layer.gamma)
+    return layer, act, gamma, Xq, xs, rand(T, E), res
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp8"])
+def test_layer_memory_comes_from_the_stream_of_the_call(fmt, monkeypatch):
+    layer, act, gamma, Xq, xs, logits, res = _layer(fmt)
+    want = [t.clone() for t in layer.forward(Xq, xs, logits, res)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    seen = _Allocations(monkeypatch)
+    layer.prepare(act, 0.5, gamma, stream=side)
+    got = layer.forward(Xq, xs, logits, res, stream=side)
+    side.synchronize()
+    assert len(seen.streams) > 10 and all(s == side for s in seen.streams)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp8"])
+def test_layer_passes_in_a_row_beside_the_caller_stream(fmt):
+    """Passes on a side stream without a wait between them, while the caller's stream allocates,
+    overwrites and frees blocks of the stages' sizes."""
+    layer, act, gamma, Xq, xs, logits, res = _layer(fmt, T=2000, H=512, I=512)
+    want = [t.clone() for t in layer.forward(Xq, xs, logits, res)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    outs = []
+    for _ in range(20):
+        outs.append(layer.forward(Xq, xs, logits, res, stream=side))
+        for n in (2000 * 2 * 1024 * 2, 2000 * 2 * 512, 2000 * 2 * 4):
+            torch.empty(n, dtype=torch.uint8, device="cuda").fill_(255)
+    torch.cuda.synchronize()
+    for got in outs:
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)

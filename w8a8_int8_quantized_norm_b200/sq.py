@@ -191,6 +191,27 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+# The current stream's handle and the current device, without building the
+# Python objects around them: a single-token call costs about as much host time
+# as these do (3.2 us of torch.cuda.current_stream() against 0.1 us).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_NO_SCOPE = contextlib.nullcontext()
+
+
+def _scope(device: torch.device, stream):
+    """The context of a call on tensors of ``device``: that device current, and
+    what the call allocates taken from the memory of the stream it runs on."""
+    if device.type != "cuda":  # the call itself refuses such tensors
+        return _NO_SCOPE
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, device))
+        return torch.cuda.stream(stream)
+    return _NO_SCOPE if _raw_device() == device.index else torch.cuda.device(device)
+
+
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -229,12 +250,14 @@ def _vec(t: Optional[torch.Tensor], K: int, name: str):
 def calibrate_absmax(x: torch.Tensor, norm: int, gamma=None, beta=None, eps: float = 1e-5,
                      act_max: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     M, K, ld = _rows(x, "x")
-    if act_max is None:
-        act_max = torch.zeros(K, dtype=torch.float32, device=x.device)
-    _vec(act_max, K, "act_max")
-    _check(lib().sq_calibrate_absmax(_ptr(x), _dtype_code(x), M, K, ld, norm,
-                                     _ptr(_vec(gamma, K, "gamma")), _ptr(_vec(beta, K, "beta")),
-                                     eps, _ptr(act_max), _stream(stream)), "sq_calibrate_absmax")
+    with _scope(x.device, stream):
+        if act_max is None:
+            act_max = torch.zeros(K, dtype=torch.float32, device=x.device)
+        _vec(act_max, K, "act_max")
+        _check(lib().sq_calibrate_absmax(_ptr(x), _dtype_code(x), M, K, ld, norm,
+                                         _ptr(_vec(gamma, K, "gamma")), _ptr(_vec(beta, K, "beta")),
+                                         eps, _ptr(act_max), _stream(stream)),
+               "sq_calibrate_absmax")
     return act_max
 
 
@@ -252,18 +275,19 @@ def compute_smooth_scales(act_max: torch.Tensor, weights: Sequence[torch.Tensor]
     ptrs = (ctypes.c_void_p * len(weights))(*[w.data_ptr() for w in weights])
     ns = (ctypes.c_int64 * len(weights))(*[w.shape[0] for w in weights])
     dev = act_max.device
-    s = torch.empty(K, dtype=torch.float32, device=dev) if s is None else _vec(s, K, "s")
-    gf = (torch.empty(K, dtype=torch.float32, device=dev) if gamma_folded is None
-          else _vec(gamma_folded, K, "gamma_folded"))
-    bf = None
-    if beta is not None:
-        bf = (torch.empty(K, dtype=torch.float32, device=dev) if beta_folded is None
-              else _vec(beta_folded, K, "beta_folded"))
-    _check(lib().sq_compute_smooth_scales(_ptr(act_max), ctypes.cast(ptrs, ctypes.c_void_p),
-                                          ctypes.cast(ns, ctypes.c_void_p), len(weights), dt, K,
-                                          float(alpha), clamp_eps, _ptr(_vec(gamma, K, "gamma")),
-                                          _ptr(_vec(beta, K, "beta")), _ptr(s), _ptr(gf), _ptr(bf),
-                                          _stream(stream)), "sq_compute_smooth_scales")
+    with _scope(dev, stream):
+        s = torch.empty(K, dtype=torch.float32, device=dev) if s is None else _vec(s, K, "s")
+        gf = (torch.empty(K, dtype=torch.float32, device=dev) if gamma_folded is None
+              else _vec(gamma_folded, K, "gamma_folded"))
+        bf = None
+        if beta is not None:
+            bf = (torch.empty(K, dtype=torch.float32, device=dev) if beta_folded is None
+                  else _vec(beta_folded, K, "beta_folded"))
+        _check(lib().sq_compute_smooth_scales(
+            _ptr(act_max), ctypes.cast(ptrs, ctypes.c_void_p), ctypes.cast(ns, ctypes.c_void_p),
+            len(weights), dt, K, float(alpha), clamp_eps, _ptr(_vec(gamma, K, "gamma")),
+            _ptr(_vec(beta, K, "beta")), _ptr(s), _ptr(gf), _ptr(bf), _stream(stream)),
+            "sq_compute_smooth_scales")
     return s, gf, bf
 
 
@@ -277,12 +301,13 @@ def weight_column_max(weights: Sequence[torch.Tensor], w_max=None, stream=None) 
             raise ValueError("weights must be contiguous [N, K] of one dtype")
     ptrs = (ctypes.c_void_p * len(weights))(*[w.data_ptr() for w in weights])
     ns = (ctypes.c_int64 * len(weights))(*[w.shape[0] for w in weights])
-    if w_max is None:
-        w_max = torch.empty(K, dtype=torch.float32, device=weights[0].device)
-    _check(lib().sq_weight_column_max(ctypes.cast(ptrs, ctypes.c_void_p),
-                                      ctypes.cast(ns, ctypes.c_void_p), len(weights), dt, K,
-                                      _ptr(_vec(w_max, K, "w_max")), _stream(stream)),
-           "sq_weight_column_max")
+    with _scope(weights[0].device, stream):
+        if w_max is None:
+            w_max = torch.empty(K, dtype=torch.float32, device=weights[0].device)
+        _check(lib().sq_weight_column_max(ctypes.cast(ptrs, ctypes.c_void_p),
+                                          ctypes.cast(ns, ctypes.c_void_p), len(weights), dt, K,
+                                          _ptr(_vec(w_max, K, "w_max")), _stream(stream)),
+               "sq_weight_column_max")
     return w_max
 
 
@@ -292,29 +317,33 @@ def smooth_scales_from_maxima(act_max: torch.Tensor, w_max: torch.Tensor, alpha:
     """s, gamma / s and beta / s from the two maxima (s may be w_max)."""
     K = act_max.numel()
     dev = act_max.device
-    s = torch.empty(K, dtype=torch.float32, device=dev) if s is None else s
-    gf = torch.empty(K, dtype=torch.float32, device=dev) if gamma_folded is None else gamma_folded
-    bf = None
-    if beta is not None:
-        bf = torch.empty(K, dtype=torch.float32, device=dev) if beta_folded is None else beta_folded
-    _check(lib().sq_smooth_scales_from_maxima(
-        _ptr(_vec(act_max, K, "act_max")), _ptr(_vec(w_max, K, "w_max")), K, float(alpha),
-        clamp_eps, _ptr(_vec(gamma, K, "gamma")), _ptr(_vec(beta, K, "beta")),
-        _ptr(_vec(s, K, "s")), _ptr(_vec(gf, K, "gamma_folded")),
-        _ptr(_vec(bf, K, "beta_folded")), _stream(stream)), "sq_smooth_scales_from_maxima")
+    with _scope(dev, stream):
+        s = torch.empty(K, dtype=torch.float32, device=dev) if s is None else s
+        gf = (torch.empty(K, dtype=torch.float32, device=dev) if gamma_folded is None
+              else gamma_folded)
+        bf = None
+        if beta is not None:
+            bf = (torch.empty(K, dtype=torch.float32, device=dev) if beta_folded is None
+                  else beta_folded)
+        _check(lib().sq_smooth_scales_from_maxima(
+            _ptr(_vec(act_max, K, "act_max")), _ptr(_vec(w_max, K, "w_max")), K, float(alpha),
+            clamp_eps, _ptr(_vec(gamma, K, "gamma")), _ptr(_vec(beta, K, "beta")),
+            _ptr(_vec(s, K, "s")), _ptr(_vec(gf, K, "gamma_folded")),
+            _ptr(_vec(bf, K, "beta_folded")), _stream(stream)), "sq_smooth_scales_from_maxima")
     return s, gf, bf
 
 
 def smooth_quantize_weights(W: torch.Tensor, s: Optional[torch.Tensor] = None, Wq=None,
                             w_scale=None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     N, K, ld = _rows(W, "W")
-    if Wq is None:
-        Wq = torch.empty((N, K), dtype=torch.int8, device=W.device)
-    if w_scale is None:
-        w_scale = torch.empty(N, dtype=torch.float32, device=W.device)
-    _check(lib().sq_smooth_quantize_weights(_ptr(W), _dtype_code(W), N, K, ld,
-                                            _ptr(_vec(s, K, "s")), _ptr(Wq), _ptr(w_scale),
-                                            _stream(stream)), "sq_smooth_quantize_weights")
+    with _scope(W.device, stream):
+        if Wq is None:
+            Wq = torch.empty((N, K), dtype=torch.int8, device=W.device)
+        if w_scale is None:
+            w_scale = torch.empty(N, dtype=torch.float32, device=W.device)
+        _check(lib().sq_smooth_quantize_weights(_ptr(W), _dtype_code(W), N, K, ld,
+                                                _ptr(_vec(s, K, "s")), _ptr(Wq), _ptr(w_scale),
+                                                _stream(stream)), "sq_smooth_quantize_weights")
     return Wq, w_scale
 
 
@@ -322,14 +351,15 @@ def norm_smooth_quant_per_token(x: torch.Tensor, norm: int, gamma_folded=None, b
                                 eps: float = 1e-5, Xq=None, x_scale=None, stream=None
                                 ) -> Tuple[torch.Tensor, torch.Tensor]:
     M, K, ld = _rows(x, "x")
-    if Xq is None:
-        Xq = torch.empty((M, K), dtype=torch.int8, device=x.device)
-    if x_scale is None:
-        x_scale = torch.empty(M, dtype=torch.float32, device=x.device)
-    _check(lib().sq_norm_smooth_quant_per_token(
-        _ptr(x), _dtype_code(x), M, K, ld, norm, _ptr(_vec(gamma_folded, K, "gamma_folded")),
-        _ptr(_vec(beta_folded, K, "beta_folded")), eps, _ptr(Xq), _ptr(x_scale), _stream(stream)),
-        "sq_norm_smooth_quant_per_token")
+    with _scope(x.device, stream):
+        if Xq is None:
+            Xq = torch.empty((M, K), dtype=torch.int8, device=x.device)
+        if x_scale is None:
+            x_scale = torch.empty(M, dtype=torch.float32, device=x.device)
+        _check(lib().sq_norm_smooth_quant_per_token(
+            _ptr(x), _dtype_code(x), M, K, ld, norm, _ptr(_vec(gamma_folded, K, "gamma_folded")),
+            _ptr(_vec(beta_folded, K, "beta_folded")), eps, _ptr(Xq), _ptr(x_scale),
+            _stream(stream)), "sq_norm_smooth_quant_per_token")
     return Xq, x_scale
 
 
@@ -337,12 +367,13 @@ def norm_smooth_absmax(x: torch.Tensor, norm: int, gamma_folded=None, beta_folde
                        eps: float = 1e-5, absmax=None, stream=None) -> torch.Tensor:
     """Running max over all of |norm(x)| into a 1-element fp32 device tensor."""
     M, K, ld = _rows(x, "x")
-    if absmax is None:
-        absmax = torch.zeros(1, dtype=torch.float32, device=x.device)
-    _check(lib().sq_norm_smooth_absmax(_ptr(x), _dtype_code(x), M, K, ld, norm,
-                                       _ptr(_vec(gamma_folded, K, "gamma_folded")),
-                                       _ptr(_vec(beta_folded, K, "beta_folded")), eps,
-                                       _ptr(absmax), _stream(stream)), "sq_norm_smooth_absmax")
+    with _scope(x.device, stream):
+        if absmax is None:
+            absmax = torch.zeros(1, dtype=torch.float32, device=x.device)
+        _check(lib().sq_norm_smooth_absmax(_ptr(x), _dtype_code(x), M, K, ld, norm,
+                                           _ptr(_vec(gamma_folded, K, "gamma_folded")),
+                                           _ptr(_vec(beta_folded, K, "beta_folded")), eps,
+                                           _ptr(absmax), _stream(stream)), "sq_norm_smooth_absmax")
     return absmax
 
 
@@ -351,14 +382,15 @@ def norm_smooth_quant_per_tensor(x: torch.Tensor, norm: int, absmax: torch.Tenso
                                  Xq=None, x_scale=None, stream=None):
     """Codes with the one step fl32(absmax / 127); x_scale holds it per row."""
     M, K, ld = _rows(x, "x")
-    if Xq is None:
-        Xq = torch.empty((M, K), dtype=torch.int8, device=x.device)
-    if x_scale is None:
-        x_scale = torch.empty(M, dtype=torch.float32, device=x.device)
-    _check(lib().sq_norm_smooth_quant_per_tensor(
-        _ptr(x), _dtype_code(x), M, K, ld, norm, _ptr(_vec(gamma_folded, K, "gamma_folded")),
-        _ptr(_vec(beta_folded, K, "beta_folded")), eps, _ptr(absmax), _ptr(Xq), _ptr(x_scale),
-        _stream(stream)), "sq_norm_smooth_quant_per_tensor")
+    with _scope(x.device, stream):
+        if Xq is None:
+            Xq = torch.empty((M, K), dtype=torch.int8, device=x.device)
+        if x_scale is None:
+            x_scale = torch.empty(M, dtype=torch.float32, device=x.device)
+        _check(lib().sq_norm_smooth_quant_per_tensor(
+            _ptr(x), _dtype_code(x), M, K, ld, norm, _ptr(_vec(gamma_folded, K, "gamma_folded")),
+            _ptr(_vec(beta_folded, K, "beta_folded")), eps, _ptr(absmax), _ptr(Xq), _ptr(x_scale),
+            _stream(stream)), "sq_norm_smooth_quant_per_tensor")
     return Xq, x_scale
 
 
@@ -366,23 +398,25 @@ def quant_per_token_given_absmax(x: torch.Tensor, row_absmax: torch.Tensor, Xq=N
                                  x_scale=None, stream=None):
     """Per-token codes of x [M, K] with each row's max |x| given (no norm)."""
     M, K, ld = _rows(x, "x")
-    if Xq is None:
-        Xq = torch.empty((M, K), dtype=torch.int8, device=x.device)
-    if x_scale is None:
-        x_scale = torch.empty(M, dtype=torch.float32, device=x.device)
-    _check(lib().sq_quant_per_token_given_absmax(
-        _ptr(x), _dtype_code(x), M, K, ld, _ptr(_vec(row_absmax, M, "row_absmax")), _ptr(Xq),
-        _ptr(x_scale), _stream(stream)), "sq_quant_per_token_given_absmax")
+    with _scope(x.device, stream):
+        if Xq is None:
+            Xq = torch.empty((M, K), dtype=torch.int8, device=x.device)
+        if x_scale is None:
+            x_scale = torch.empty(M, dtype=torch.float32, device=x.device)
+        _check(lib().sq_quant_per_token_given_absmax(
+            _ptr(x), _dtype_code(x), M, K, ld, _ptr(_vec(row_absmax, M, "row_absmax")), _ptr(Xq),
+            _ptr(x_scale), _stream(stream)), "sq_quant_per_token_given_absmax")
     return Xq, x_scale
 
 
 def row_absmax(x: torch.Tensor, out=None, stream=None) -> torch.Tensor:
     """max_k |x[m, k]| per row of x [M, K] (no norm), fp32 [M]."""
     M, K, ld = _rows(x, "x")
-    if out is None:
-        out = torch.empty(M, dtype=torch.float32, device=x.device)
-    _check(lib().sq_row_absmax(_ptr(x), _dtype_code(x), M, K, ld, _ptr(_vec(out, M, "out")),
-                               _stream(stream)), "sq_row_absmax")
+    with _scope(x.device, stream):
+        if out is None:
+            out = torch.empty(M, dtype=torch.float32, device=x.device)
+        _check(lib().sq_row_absmax(_ptr(x), _dtype_code(x), M, K, ld, _ptr(_vec(out, M, "out")),
+                                   _stream(stream)), "sq_row_absmax")
     return out
 
 
@@ -394,15 +428,16 @@ def dequant_i32(acc: torch.Tensor, x_scale: torch.Tensor, w_scale: torch.Tensor,
     M, N = acc.shape
     if epi not in ("bf16", "bf16_relu"):
         raise ValueError("epi must be bf16 or bf16_relu")
-    if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=acc.device)
-    if tuple(out.shape) != (M, N) or out.dtype != torch.bfloat16 or \
-            (N > 1 and out.stride(1) != 1):
-        raise ValueError("out must be a bf16 [M, N] tensor with unit column stride")
-    _check(lib().sq_dequant_i32(_ptr(acc), M, N, max(acc.stride(0), N),
-                                _ptr(_vec(x_scale, M, "x_scale")), _ptr(_vec(w_scale, N, "w_scale")),
-                                EPI[epi], _ptr(out), max(out.stride(0), N), _stream(stream)),
-           "sq_dequant_i32")
+    with _scope(acc.device, stream):
+        if out is None:
+            out = torch.empty((M, N), dtype=torch.bfloat16, device=acc.device)
+        if tuple(out.shape) != (M, N) or out.dtype != torch.bfloat16 or \
+                (N > 1 and out.stride(1) != 1):
+            raise ValueError("out must be a bf16 [M, N] tensor with unit column stride")
+        _check(lib().sq_dequant_i32(_ptr(acc), M, N, max(acc.stride(0), N),
+                                    _ptr(_vec(x_scale, M, "x_scale")),
+                                    _ptr(_vec(w_scale, N, "w_scale")), EPI[epi], _ptr(out),
+                                    max(out.stride(0), N), _stream(stream)), "sq_dequant_i32")
     return out
 
 
@@ -413,17 +448,18 @@ def llmint8_outliers(col_absmax: torch.Tensor, tau: float = 6.0, mask=None, idx=
     channels ascending (count stays on the device)."""
     K = col_absmax.numel()
     dev = col_absmax.device
-    if mask is None:
-        mask = torch.empty(K, dtype=torch.float32, device=dev)
-    if idx is None:
-        idx = torch.empty(K, dtype=torch.int32, device=dev)
-    if count is None:
-        count = torch.empty(1, dtype=torch.int32, device=dev)
-    if idx.dtype != torch.int32 or idx.numel() < K or count.dtype != torch.int32:
-        raise ValueError("idx [K] and count [1] must be int32")
-    _check(lib().sq_llmint8_outliers(_ptr(_vec(col_absmax, K, "col_absmax")), K, tau,
-                                     _ptr(_vec(mask, K, "mask")), _ptr(idx), _ptr(count),
-                                     _stream(stream)), "sq_llmint8_outliers")
+    with _scope(dev, stream):
+        if mask is None:
+            mask = torch.empty(K, dtype=torch.float32, device=dev)
+        if idx is None:
+            idx = torch.empty(K, dtype=torch.int32, device=dev)
+        if count is None:
+            count = torch.empty(1, dtype=torch.int32, device=dev)
+        if idx.dtype != torch.int32 or idx.numel() < K or count.dtype != torch.int32:
+            raise ValueError("idx [K] and count [1] must be int32")
+        _check(lib().sq_llmint8_outliers(_ptr(_vec(col_absmax, K, "col_absmax")), K, tau,
+                                         _ptr(_vec(mask, K, "mask")), _ptr(idx), _ptr(count),
+                                         _stream(stream)), "sq_llmint8_outliers")
     return mask, idx, count
 
 
@@ -437,14 +473,15 @@ def llmint8_combine(acc: torch.Tensor, x_scale, w_scale, x: torch.Tensor, W: tor
     if Kw != K or W.shape[0] != N or acc.dtype != torch.int32 or \
             (N > 1 and acc.stride(1) != 1):
         raise ValueError("acc [M, N] int32, x [M, K], W [N, K]")
-    if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=acc.device)
-    _check(lib().sq_llmint8_combine(_ptr(acc), M, N, max(acc.stride(0), N),
-                                    _ptr(_vec(x_scale, M, "x_scale")),
-                                    _ptr(_vec(w_scale, N, "w_scale")), _ptr(x), _dtype_code(x),
-                                    ldx, _ptr(W), _dtype_code(W), ldw, K, _ptr(idx), _ptr(count),
-                                    EPI[epi], _ptr(out), max(out.stride(0), N), _stream(stream)),
-           "sq_llmint8_combine")
+    with _scope(acc.device, stream):
+        if out is None:
+            out = torch.empty((M, N), dtype=torch.bfloat16, device=acc.device)
+        _check(lib().sq_llmint8_combine(_ptr(acc), M, N, max(acc.stride(0), N),
+                                        _ptr(_vec(x_scale, M, "x_scale")),
+                                        _ptr(_vec(w_scale, N, "w_scale")), _ptr(x), _dtype_code(x),
+                                        ldx, _ptr(W), _dtype_code(W), ldw, K, _ptr(idx),
+                                        _ptr(count), EPI[epi], _ptr(out), max(out.stride(0), N),
+                                        _stream(stream)), "sq_llmint8_combine")
     return out
 
 
@@ -457,18 +494,20 @@ def silu_mul_quant_per_token(gate_up: torch.Tensor, Xq=None, x_scale=None, h_out
     if K2 % 2:
         raise ValueError("gate_up rows hold two halves")
     I = K2 // 2
-    if Xq is None:
-        Xq = torch.empty((M, I), dtype=torch.uint8 if fp8 else torch.int8, device=gate_up.device)
-    if x_scale is None:
-        x_scale = torch.empty(M, dtype=torch.float32, device=gate_up.device)
-    ldh = 0
-    if h_out is not None:
-        if h_out.dtype != torch.bfloat16 or tuple(h_out.shape) != (M, I):
-            raise ValueError("h_out must be bf16 [M, I]")
-        _, _, ldh = _rows(h_out, "h_out")
-    call = "sq_silu_mul_quant_per_token_fp8" if fp8 else "sq_silu_mul_quant_per_token"
-    _check(getattr(lib(), call)(_ptr(gate_up), _dtype_code(gate_up), M, I, ld, _ptr(Xq),
-                                _ptr(x_scale), _ptr(h_out), ldh, _stream(stream)), call)
+    with _scope(gate_up.device, stream):
+        if Xq is None:
+            Xq = torch.empty((M, I), dtype=torch.uint8 if fp8 else torch.int8,
+                             device=gate_up.device)
+        if x_scale is None:
+            x_scale = torch.empty(M, dtype=torch.float32, device=gate_up.device)
+        ldh = 0
+        if h_out is not None:
+            if h_out.dtype != torch.bfloat16 or tuple(h_out.shape) != (M, I):
+                raise ValueError("h_out must be bf16 [M, I]")
+            _, _, ldh = _rows(h_out, "h_out")
+        call = "sq_silu_mul_quant_per_token_fp8" if fp8 else "sq_silu_mul_quant_per_token"
+        _check(getattr(lib(), call)(_ptr(gate_up), _dtype_code(gate_up), M, I, ld, _ptr(Xq),
+                                    _ptr(x_scale), _ptr(h_out), ldh, _stream(stream)), call)
     return Xq, x_scale
 
 
@@ -478,27 +517,30 @@ def norm_smooth_quant_per_token_fp8(x: torch.Tensor, norm: int, gamma_folded=Non
                                     beta_folded=None, eps: float = 1e-5, Xq8=None, x_scale=None,
                                     stream=None):
     M, K, ld = _rows(x, "x")
-    if Xq8 is None:
-        Xq8 = torch.empty((M, K), dtype=torch.uint8, device=x.device)
-    if x_scale is None:
-        x_scale = torch.empty(M, dtype=torch.float32, device=x.device)
-    _check(lib().sq_norm_smooth_quant_per_token_fp8(
-        _ptr(x), _dtype_code(x), M, K, ld, norm, _ptr(_vec(gamma_folded, K, "gamma_folded")),
-        _ptr(_vec(beta_folded, K, "beta_folded")), eps, _ptr(Xq8), _ptr(x_scale),
-        _stream(stream)), "sq_norm_smooth_quant_per_token_fp8")
+    with _scope(x.device, stream):
+        if Xq8 is None:
+            Xq8 = torch.empty((M, K), dtype=torch.uint8, device=x.device)
+        if x_scale is None:
+            x_scale = torch.empty(M, dtype=torch.float32, device=x.device)
+        _check(lib().sq_norm_smooth_quant_per_token_fp8(
+            _ptr(x), _dtype_code(x), M, K, ld, norm, _ptr(_vec(gamma_folded, K, "gamma_folded")),
+            _ptr(_vec(beta_folded, K, "beta_folded")), eps, _ptr(Xq8), _ptr(x_scale),
+            _stream(stream)), "sq_norm_smooth_quant_per_token_fp8")
     return Xq8, x_scale
 
 
 def smooth_quantize_weights_fp8(W: torch.Tensor, s: Optional[torch.Tensor] = None, Wq8=None,
                                 w_scale=None, stream=None):
     N, K, ld = _rows(W, "W")
-    if Wq8 is None:
-        Wq8 = torch.empty((N, K), dtype=torch.uint8, device=W.device)
-    if w_scale is None:
-        w_scale = torch.empty(N, dtype=torch.float32, device=W.device)
-    _check(lib().sq_smooth_quantize_weights_fp8(_ptr(W), _dtype_code(W), N, K, ld,
-                                                _ptr(_vec(s, K, "s")), _ptr(Wq8), _ptr(w_scale),
-                                                _stream(stream)), "sq_smooth_quantize_weights_fp8")
+    with _scope(W.device, stream):
+        if Wq8 is None:
+            Wq8 = torch.empty((N, K), dtype=torch.uint8, device=W.device)
+        if w_scale is None:
+            w_scale = torch.empty(N, dtype=torch.float32, device=W.device)
+        _check(lib().sq_smooth_quantize_weights_fp8(_ptr(W), _dtype_code(W), N, K, ld,
+                                                    _ptr(_vec(s, K, "s")), _ptr(Wq8), _ptr(w_scale),
+                                                    _stream(stream)),
+               "sq_smooth_quantize_weights_fp8")
     return Wq8, w_scale
 
 
@@ -513,34 +555,36 @@ def fp8_gemm_dequant(Xq8: torch.Tensor, Wq8: torch.Tensor, x_scale: Optional[tor
     if Xq8.dtype != torch.uint8 or Wq8.dtype != torch.uint8 or not Xq8.is_contiguous() \
             or not Wq8.is_contiguous() or Wq8.shape[1] != K:
         raise ValueError("Xq8 [M,K] and Wq8 [N,K] must be contiguous uint8 (e4m3 bytes)")
-    if out is None:
-        out = torch.empty((M, N), dtype=torch.float32 if epi == "f32" else torch.bfloat16,
-                          device=Xq8.device)
-    if whole_k:
-        workspace = None
-    else:
-        need = gemm_workspace_size(M, N, K, 0) if path_hint != 1 and path_hint != 3 else 0
-        if workspace is None and need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=Xq8.device)
-    wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check(lib().sq_fp8_gemm_dequant(_ptr(Xq8), _ptr(Wq8), _ptr(x_scale), _ptr(w_scale), M, N, K,
-                                     EPI[epi], _ptr(out), out.stride(0), _ptr(workspace), wsb,
-                                     path_hint, _stream(stream)), "sq_fp8_gemm_dequant")
+    with _scope(Xq8.device, stream):
+        if out is None:
+            out = torch.empty((M, N), dtype=torch.float32 if epi == "f32" else torch.bfloat16,
+                              device=Xq8.device)
+        if whole_k:
+            workspace = None
+        else:
+            need = gemm_workspace_size(M, N, K, 0) if path_hint != 1 and path_hint != 3 else 0
+            if workspace is None and need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=Xq8.device)
+        wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
+        _check(lib().sq_fp8_gemm_dequant(_ptr(Xq8), _ptr(Wq8), _ptr(x_scale), _ptr(w_scale), M, N,
+                                         K, EPI[epi], _ptr(out), out.stride(0), _ptr(workspace), wsb,
+                                         path_hint, _stream(stream)), "sq_fp8_gemm_dequant")
     return out
 
 
 def smooth_quantize_weights_per_tensor(W: torch.Tensor, s: Optional[torch.Tensor] = None,
                                        Wq=None, w_scale=None, w_absmax=None, stream=None):
     N, K, ld = _rows(W, "W")
-    if Wq is None:
-        Wq = torch.empty((N, K), dtype=torch.int8, device=W.device)
-    if w_scale is None:
-        w_scale = torch.empty(N, dtype=torch.float32, device=W.device)
-    if w_absmax is None:
-        w_absmax = torch.empty(1, dtype=torch.float32, device=W.device)
-    _check(lib().sq_smooth_quantize_weights_per_tensor(
-        _ptr(W), _dtype_code(W), N, K, ld, _ptr(_vec(s, K, "s")), _ptr(Wq), _ptr(w_scale),
-        _ptr(w_absmax), _stream(stream)), "sq_smooth_quantize_weights_per_tensor")
+    with _scope(W.device, stream):
+        if Wq is None:
+            Wq = torch.empty((N, K), dtype=torch.int8, device=W.device)
+        if w_scale is None:
+            w_scale = torch.empty(N, dtype=torch.float32, device=W.device)
+        if w_absmax is None:
+            w_absmax = torch.empty(1, dtype=torch.float32, device=W.device)
+        _check(lib().sq_smooth_quantize_weights_per_tensor(
+            _ptr(W), _dtype_code(W), N, K, ld, _ptr(_vec(s, K, "s")), _ptr(Wq), _ptr(w_scale),
+            _ptr(w_absmax), _stream(stream)), "sq_smooth_quantize_weights_per_tensor")
     return Wq, w_scale
 
 
@@ -565,17 +609,18 @@ def w8a8_gemm_dequant(Xq: torch.Tensor, Wq: torch.Tensor, x_scale: Optional[torc
             or not Wq.is_contiguous() or Wq.shape[1] != K:
         raise ValueError("Xq [M,K] and Wq [N,K] must be contiguous int8")
     code = EPI[epi]
-    if out is None:
-        out = torch.empty((M, N), dtype=torch.int32 if epi == "i32" else torch.bfloat16,
-                          device=Xq.device)
-    need = gemm_workspace_size(M, N, K, split_k)
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=Xq.device)
-    wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check(lib().sq_w8a8_gemm_dequant(_ptr(Xq), _ptr(Wq), _ptr(x_scale), _ptr(w_scale), M, N, K,
-                                      code, _ptr(out), out.stride(0), _ptr(workspace), wsb,
-                                      path_hint, split_k, _stream(stream)),
-           "sq_w8a8_gemm_dequant")
+    with _scope(Xq.device, stream):
+        if out is None:
+            out = torch.empty((M, N), dtype=torch.int32 if epi == "i32" else torch.bfloat16,
+                              device=Xq.device)
+        need = gemm_workspace_size(M, N, K, split_k)
+        if workspace is None and need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=Xq.device)
+        wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
+        _check(lib().sq_w8a8_gemm_dequant(_ptr(Xq), _ptr(Wq), _ptr(x_scale), _ptr(w_scale), M, N, K,
+                                          code, _ptr(out), out.stride(0), _ptr(workspace), wsb,
+                                          path_hint, split_k, _stream(stream)),
+               "sq_w8a8_gemm_dequant")
     return out
 
 
@@ -589,14 +634,15 @@ def w8a8_gemm_dequant_rowmax(Xq: torch.Tensor, Wq: torch.Tensor, x_scale: torch.
     if Xq.dtype != torch.int8 or Wq.dtype != torch.int8 or not Xq.is_contiguous() \
             or not Wq.is_contiguous() or Wq.shape[1] != K:
         raise ValueError("Xq [M,K] and Wq [N,K] must be contiguous int8")
-    if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=Xq.device)
-    if row_absmax is None:
-        row_absmax = torch.empty(M, dtype=torch.float32, device=Xq.device)
-    _check(lib().sq_w8a8_gemm_dequant_rowmax(
-        _ptr(Xq), _ptr(Wq), _ptr(x_scale), _ptr(w_scale), M, N, K, EPI[epi], _ptr(out),
-        out.stride(0), _ptr(_vec(row_absmax, M, "row_absmax")), path_hint, _stream(stream)),
-        "sq_w8a8_gemm_dequant_rowmax")
+    with _scope(Xq.device, stream):
+        if out is None:
+            out = torch.empty((M, N), dtype=torch.bfloat16, device=Xq.device)
+        if row_absmax is None:
+            row_absmax = torch.empty(M, dtype=torch.float32, device=Xq.device)
+        _check(lib().sq_w8a8_gemm_dequant_rowmax(
+            _ptr(Xq), _ptr(Wq), _ptr(x_scale), _ptr(w_scale), M, N, K, EPI[epi], _ptr(out),
+            out.stride(0), _ptr(_vec(row_absmax, M, "row_absmax")), path_hint, _stream(stream)),
+            "sq_w8a8_gemm_dequant_rowmax")
     return out, row_absmax
 
 
@@ -619,10 +665,11 @@ def w8a8_gemm_dequant_noalloc(Xq: torch.Tensor, Wq: torch.Tensor,
             or out.device != Xq.device or Wq.device != Xq.device):
         raise ValueError("out must be a [M, N] = [%d, %d] %s tensor with unit column stride "
                          "on the device of Xq" % (M, N, want))
-    _check(lib().sq_w8a8_gemm_dequant_noalloc(_ptr(Xq), _ptr(Wq), _ptr(x_scale), _ptr(w_scale),
-                                              M, N, K, EPI[epi], _ptr(out), out.stride(0),
-                                              path_hint, split_k, _stream(stream)),
-           "sq_w8a8_gemm_dequant_noalloc")
+    with _scope(Xq.device, stream):
+        _check(lib().sq_w8a8_gemm_dequant_noalloc(_ptr(Xq), _ptr(Wq), _ptr(x_scale), _ptr(w_scale),
+                                                  M, N, K, EPI[epi], _ptr(out), out.stride(0),
+                                                  path_hint, split_k, _stream(stream)),
+               "sq_w8a8_gemm_dequant_noalloc")
     return out
 
 
@@ -631,23 +678,24 @@ def linear_w8a8(x: torch.Tensor, norm: int, gamma_folded, beta_folded, eps: floa
                 Xq_scratch=None, xscale_scratch=None, workspace=None, stream=None) -> torch.Tensor:
     M, K, ld = _rows(x, "x")
     N = Wq.shape[0]
-    if out is None:
-        out = torch.empty((M, N), dtype=torch.int32 if epi == "i32" else torch.bfloat16,
-                          device=x.device)
-    if Xq_scratch is None:
-        Xq_scratch = torch.empty((M, K), dtype=torch.int8, device=x.device)
-    if xscale_scratch is None:
-        xscale_scratch = torch.empty(M, dtype=torch.float32, device=x.device)
-    need = gemm_workspace_size(M, N, K, 0)
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check(lib().sq_linear_w8a8(_ptr(x), _dtype_code(x), M, K, ld, norm,
-                                _ptr(_vec(gamma_folded, K, "gamma_folded")),
-                                _ptr(_vec(beta_folded, K, "beta_folded")), eps, _ptr(Wq),
-                                _ptr(w_scale), N, EPI[epi], _ptr(out), out.stride(0),
-                                _ptr(Xq_scratch), _ptr(xscale_scratch), _ptr(workspace), wsb,
-                                _stream(stream)), "sq_linear_w8a8")
+    with _scope(x.device, stream):
+        if out is None:
+            out = torch.empty((M, N), dtype=torch.int32 if epi == "i32" else torch.bfloat16,
+                              device=x.device)
+        if Xq_scratch is None:
+            Xq_scratch = torch.empty((M, K), dtype=torch.int8, device=x.device)
+        if xscale_scratch is None:
+            xscale_scratch = torch.empty(M, dtype=torch.float32, device=x.device)
+        need = gemm_workspace_size(M, N, K, 0)
+        if workspace is None and need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
+        _check(lib().sq_linear_w8a8(_ptr(x), _dtype_code(x), M, K, ld, norm,
+                                    _ptr(_vec(gamma_folded, K, "gamma_folded")),
+                                    _ptr(_vec(beta_folded, K, "beta_folded")), eps, _ptr(Wq),
+                                    _ptr(w_scale), N, EPI[epi], _ptr(out), out.stride(0),
+                                    _ptr(Xq_scratch), _ptr(xscale_scratch), _ptr(workspace), wsb,
+                                    _stream(stream)), "sq_linear_w8a8")
     return out
 
 
@@ -660,25 +708,6 @@ class MoeRoute(NamedTuple):
     offsets: torch.Tensor    # [E + 1] int32, expert e's rows are offsets[e] .. offsets[e + 1]
     row_token: torch.Tensor  # [T * top_k] int32, the token of each row
     token_row: torch.Tensor  # [T, top_k] int32, the row of each token's j-th expert, -1: none
-
-
-# The current stream's handle and the current device, without building the
-# Python objects around them: a single-token call costs about as much host time
-# as these do (3.2 us of torch.cuda.current_stream() against 0.1 us).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
-_raw_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-_NO_SCOPE = contextlib.nullcontext()
-
-
-def _scope(device: torch.device, stream):
-    """The context of a call on tensors of ``device``: that device current, and
-    what the call allocates taken from the memory of the stream it runs on."""
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, device))
-        return torch.cuda.stream(stream)
-    return _NO_SCOPE if _raw_device() == device.index else torch.cuda.device(device)
 
 
 def _dense(t: Optional[torch.Tensor], shape, dtype, device, name: str):
