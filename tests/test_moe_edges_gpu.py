@@ -1,5 +1,7 @@
 """The operators of a layer of experts at their edges: waits that run out, memory of the right
 stream, values near the ends of fp32, layouts inside one buffer."""
+import copy
+
 import numpy as np
 import pytest
 import torch
@@ -225,3 +227,70 @@ def test_layer_passes_in_a_row_beside_the_caller_stream(fmt):
     for got in outs:
         for a, b in zip(got, want):
             assert torch.equal(a, b)
+
+
+# ---------------------------------------------------------------------------
+# the layer: what a pass leaves behind
+# ---------------------------------------------------------------------------
+
+def test_layers_hold_no_stages_of_earlier_passes():
+    """A model of many layers, each pass fed by the one before: the stages of a pass go with its h,
+    so that memory does not grow with the layers."""
+    T, H, I, k = 1000, 256, 512, 2
+    layer, act, gamma, Xq, xs, logits, res = _layer("int8", T=T, H=H, I=I, top_k=k)
+    layers = [layer] + [_layer("int8", T=T, H=H, I=I, top_k=k)[0] for _ in range(7)]
+    one = T * k * (2 * I * 2 + I + H * 2)  # bytes of a pass's gate/up rows, codes and down rows
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    h, q, s = res, Xq, xs
+    for l in layers:
+        h, q, s = l.forward(q, s, logits, h)
+    assert torch.cuda.memory_allocated() - before < 2 * one
+    assert all(l.stages is None for l in layers[:-1])
+    assert layers[-1].stages is h.stages
+    assert set(h.stages) == {"route", "gate_up", "Hq", "h_scale", "down"}
+    assert copy.deepcopy(layers[-1]).stages is None
+    del h
+    assert layers[-1].stages is None
+
+
+def test_layer_without_stages_leaves_its_results_alone():
+    layer, act, gamma, Xq, xs, logits, res = _layer("fp8", keep_stages=False)
+    want = _layer("fp8")[0].forward(Xq, xs, logits, res)
+    layer.forward(Xq, xs, logits, res)
+    before = torch.cuda.memory_allocated()
+    got = layer.forward(Xq, xs, logits, res)
+    left = torch.cuda.memory_allocated() - before
+    assert left <= sum(-(-t.numel() * t.element_size() // 512) * 512 for t in got)
+    assert layer.stages is None and not hasattr(got[0], "stages")
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+def test_two_threads_on_one_layer_keep_their_own_stages():
+    import threading
+
+    layer, act, gamma, Xq, xs, logits, res = _layer("int8")
+    torch.cuda.synchronize()
+    ins = [logits, logits.flip(0).contiguous()]
+    got = [None, None]
+
+    def run(i):
+        stream = torch.cuda.Stream()
+        for _ in range(10):
+            got[i] = layer.forward(Xq, xs, ins[i], res, stream=stream)
+        stream.synchronize()
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i in range(2):
+        want = layer.forward(Xq, xs, ins[i], res)
+        for a, b in zip(got[i], want):
+            assert torch.equal(a, b)
+        mine, its = got[i][0].stages, want[0].stages
+        assert torch.equal(mine["route"].experts, its["route"].experts)
+        n = int(its["route"].offsets[-1])
+        assert torch.equal(mine["down"][:n], its["down"][:n])

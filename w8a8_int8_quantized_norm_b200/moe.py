@@ -15,6 +15,7 @@ the calls and owns the prepared weights.
 """
 from __future__ import annotations
 
+import weakref
 from typing import Optional
 
 import torch
@@ -24,14 +25,24 @@ from . import sq
 FORMATS = ("int8", "fp8")
 
 
+class Stages(dict):
+    """The stages of one pass: route, gate_up, Hq, h_scale, down."""
+
+
 class MoELayer:
     """Experts with gate_up [E, 2 I, H] (gate rows first) and down [E, H, I],
     bf16 or fp32 on the device.  ``prepare`` smooths and quantises them once;
-    ``forward`` runs a batch of tokens."""
+    ``forward`` runs a batch of tokens.
+
+    The layer holds no pass's tensors.  A pass's stages are ``h.stages`` of the h
+    it returned and are freed with it; ``layer.stages`` finds those of the
+    layer's last pass while they live (else None).  With ``keep_stages`` False
+    they are freed within the pass, each as soon as the next one is computed."""
 
     def __init__(self, gate_up: torch.Tensor, down: torch.Tensor, top_k: int,
                  score: str = "softmax", bias: Optional[torch.Tensor] = None,
-                 renormalize: bool = True, scale: float = 1.0, fmt: str = "int8"):
+                 renormalize: bool = True, scale: float = 1.0, fmt: str = "int8",
+                 keep_stages: bool = True):
         E, I2, H = gate_up.shape
         if I2 % 2 or tuple(down.shape) != (E, H, I2 // 2):
             raise ValueError("gate_up must be [E, 2 I, H] and down [E, H, I]")
@@ -44,6 +55,14 @@ class MoELayer:
         self.top_k, self.score, self.bias = top_k, score, bias
         self.renormalize, self.scale, self.fmt = renormalize, float(scale), fmt
         self.s = self.gamma = self.beta = None
+        self.keep_stages, self._last = keep_stages, None
+
+    @property
+    def stages(self) -> Optional[Stages]:
+        return self._last() if self._last is not None else None
+
+    def __getstate__(self):  # a copied or saved layer has run no pass
+        return dict(self.__dict__, _last=None)
 
     def prepare(self, act_max: Optional[torch.Tensor] = None, alpha: float = 0.5, gamma=None,
                 beta=None, stream=None) -> "MoELayer":
@@ -73,16 +92,26 @@ class MoELayer:
         / ``self.beta``) and the router's logits [T, E] -> (h, codes, scales) of
         sq.block_norm_quant_per_token: h = residual_scale * residual + post_norm(sum
         of the experts) * gate ..., and the next norm's codes.  ``block`` are that
-        call's norms, gates and outputs.  The stages stay in ``self.stages``."""
+        call's norms, gates and outputs.  The stages are ``h.stages``."""
         gemm = sq.w8a8_gemm_grouped if self.fmt == "int8" else sq.fp8_gemm_grouped
         r = sq.moe_route(logits, self.top_k, self.score, self.bias, self.renormalize, self.scale,
                          stream=stream)
+        stages = Stages(route=r)
         gu = gemm(Xq, self.gate_up_q, x_scale, self.gate_up_scale, r.offsets,
                   row_token=r.row_token, stream=stream)
         # rows behind the last expert's hold no values; theirs are never read
         hq, hs = sq.silu_mul_quant_per_token(gu, stream=stream, fp8=self.fmt == "fp8")
+        if self.keep_stages:
+            stages.update(gate_up=gu, Hq=hq, h_scale=hs)
+        del gu
         y = gemm(hq, self.down_q, hs, self.down_scale, r.offsets, stream=stream)
-        self.stages = {"route": r, "gate_up": gu, "Hq": hq, "h_scale": hs, "down": y}
-        return sq.block_norm_quant_per_token(y, residual, token_row=r.token_row,
-                                             weights=r.weights, fp8=self.fmt == "fp8",
-                                             stream=stream, **block)
+        if self.keep_stages:
+            stages.update(down=y)
+        del hq, hs
+        out = sq.block_norm_quant_per_token(y, residual, token_row=r.token_row, weights=r.weights,
+                                            fp8=self.fmt == "fp8", stream=stream, **block)
+        self._last = None
+        if self.keep_stages:
+            out[0].stages = stages
+            self._last = weakref.ref(stages)
+        return out
