@@ -294,3 +294,28 @@ def test_two_threads_on_one_layer_keep_their_own_stages():
         assert torch.equal(mine["route"].experts, its["route"].experts)
         n = int(its["route"].offsets[-1])
         assert torch.equal(mine["down"][:n], its["down"][:n])
+
+
+# ---------------------------------------------------------------------------
+# matrices without rows
+# ---------------------------------------------------------------------------
+
+def test_a_matrix_without_rows_has_no_stride():
+    """numpy's empty arrays have strides of 0: no rows, so nothing is refused and nothing written.
+    With rows the columns still have to follow one another."""
+    x = torch.from_numpy(np.empty((0, 64), np.float32)).cuda()
+    odd = torch.empty_strided((0, 64), (1, 7), dtype=torch.float32, device="cuda")
+    for t in (x, odd):
+        q, s = sq.norm_smooth_quant_per_token(t, sq.NORM_RMS)
+        assert q.shape == (0, 64) and s.shape == (0,)
+        assert sq.row_absmax(t).shape == (0,)
+        q, s = sq.silu_mul_quant_per_token(t.to(torch.bfloat16))
+        assert q.shape == (0, 32) and s.shape == (0,)
+        h, q, s = sq.block_norm_quant_per_token(t)
+        assert h.shape == q.shape == (0, 64) and s.shape == (0,)
+        assert (sq.moe_route(t, 2).offsets == 0).all()
+    strided = torch.zeros((4, 128), device="cuda")[:, ::2]
+    for call in (lambda: sq.norm_smooth_quant_per_token(strided, sq.NORM_RMS), lambda: sq.row_absmax(strided),
+                 lambda: sq.block_norm_quant_per_token(strided), lambda: sq.moe_route(strided, 2)):
+        with pytest.raises(ValueError, match="unit column stride"):
+            call()

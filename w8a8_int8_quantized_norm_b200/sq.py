@@ -229,7 +229,8 @@ def _rows(t: torch.Tensor, name: str):
         raise ValueError("%s must be a CUDA tensor" % name)
     if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1 and t.shape[0] > 0):
         raise ValueError("%s must be 2-D with unit column stride" % name)
-    # a single row's stride is arbitrary (numpy / torch may report 0 for it)
+    # no row has no stride, and a single row's is arbitrary (numpy / torch may
+    # report 0 for either)
     ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
     return t.shape[0], t.shape[1], ld
 
