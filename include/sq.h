@@ -660,8 +660,10 @@ sq_status sq_w8a8_gemm_dequant_noalloc(const int8_t* Xq, const int8_t* Wq,
  *            SQ_MOE_SIGMOID: p_e = 1 / (1 + exp(-l_e))
  *   bias     device [E] fp32 or NULL; SQ_MOE_SIGMOID only: the experts are
  *            chosen by p_e + bias[e] (compared in fp64), weighted by p_e alone
- *   renormalize  non-zero: the chosen experts' weights are divided by their sum
- *            (a sum of 0 gives weights 0)
+ *   renormalize  non-zero: the chosen experts' weights are divided by their sum,
+ *            also where the scores are too small for fp32 (a sum of 0 gives
+ *            weights 0: sigmoid scores of logits below -708, where 64 bits end,
+ *            count as 0)
  *   scale    multiplies every weight (finite)
  *   weights  device [T, top_k] fp32 OUT;  experts device [T, top_k] int32 OUT,
  *            in descending order of choice, equal ones by the lower index

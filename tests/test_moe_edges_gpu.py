@@ -319,3 +319,44 @@ def test_a_matrix_without_rows_has_no_stride():
                  lambda: sq.block_norm_quant_per_token(strided), lambda: sq.moe_route(strided, 2)):
         with pytest.raises(ValueError, match="unit column stride"):
             call()
+
+
+# ---------------------------------------------------------------------------
+# router: scores below fp32's range
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("use_bias", [False, True])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_route_sigmoid_of_far_negative_logits(renorm, use_bias):
+    """Below about -88 exp(-l) overflows fp32, below -104 the score underflows; the ratios of the
+    chosen scores are ordinary numbers down to where 64 bits end (-708)."""
+    rng = _rng(1)
+    E, k = 40, 6
+    l = rng.standard_normal((12, E))
+    l[0] = rng.uniform(-100, -87, E)
+    l[1] = rng.uniform(-300, -90, E)
+    l[2] = rng.uniform(-700, -600, E)
+    l[3, :36] = -95 + rng.standard_normal(36)  # four of N(0, 1) first
+    l[4] = -88.5
+    l[5] = -200 - np.arange(E)
+    l[5, 7] = -5
+    l[6] = -1000
+    l[7] = np.finfo(np.float32).min
+    l[8] = rng.uniform(-140, -120, E)
+    l[8, 3:] = -np.inf                         # three left
+    l[9] = rng.uniform(-60, -1e-3, E)
+    l[10] = rng.uniform(60, 100, E)
+    bias = rng.standard_normal(E).astype(np.float32) if use_bias else None
+    logits = l.astype(np.float32)
+    r = sq.moe_route(_cuda_of(logits), k, score="sigmoid", bias=None if bias is None else _cuda_of(bias),
+                     renormalize=renorm, scale=2.5)
+    w, e, *_, bound = ref.route(logits.astype(np.float64), k, "sigmoid", bias, renorm, 2.5)
+    assert np.array_equal(r.experts.cpu().numpy(), e)
+    g = _np64(r.weights)
+    # a chosen score relative to the largest: exp 4 U, its argument's rounding taken back with
+    # 2 U, 1 + exp(l) 5 U, quotient 1 U; the sum 5 U, the division and the scale 2 U: 19 U, below
+    # the reference's bound (12 + E) U.  Below the normal range: a multiple of 2^-149.
+    assert (np.abs(g - w) <= bound * np.abs(w) + 2.0 ** -126).all()
+    if renorm:
+        assert np.allclose(g[[0, 1, 2, 4, 8]].sum(1), 2.5, rtol=1e-5)
+        assert (g[[6, 7]] == 0).all()  # scores of 0

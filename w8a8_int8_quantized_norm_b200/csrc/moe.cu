@@ -78,7 +78,24 @@ __device__ __forceinline__ float clean_logit(float v) {
   return v >= -FLT_MAX ? fminf(v, FLT_MAX) + 0.0f : -INFINITY;
 }
 
-__device__ __forceinline__ float sigmoid_f(float l) { return 1.0f / (1.0f + expf(-l)); }
+// 1 / (1 + exp(-l)) without an exp that overflows.
+__device__ __forceinline__ float sigmoid_f(float l) {
+  const float e = expf(-fabsf(l));
+  return (l >= 0.0f ? 1.0f : e) / (1.0f + e);
+}
+
+// Below it a sigmoid score leaves the normal range of 64 bits and counts as 0.
+constexpr float kLowestScore = -708.0f;
+
+// sigmoid(l) / sigmoid(m) up to a factor of m alone, l <= m < 0: exp(l - m) /
+// (1 + exp(l)).  The scores themselves leave fp32 below about -88, their ratios
+// do not.  l - m is rounded; what it lost is put back to first order.
+__device__ __forceinline__ float sigmoid_ratio(float l, float m) {
+  const float d = l - m, b = d - l;
+  const float lost = (l - (d - b)) - (m + b);
+  const float e = expf(d);
+  return fmaf(e, lost, e) / (1.0f + expf(l));
+}
 
 __device__ __forceinline__ float load_logit(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 __device__ __forceinline__ float load_logit(const float* p) { return *p; }
@@ -185,9 +202,18 @@ __device__ __forceinline__ void choose(const RouteParams& p, const int64_t (&t)[
     float mine = 0.0f;  // the chosen logit, from L1
     if (my_e[u] >= 0)
       mine = clean_logit(load_logit(static_cast<const T*>(p.logits) + t[u] * p.ld + my_e[u]));
-    const float m = __shfl_sync(~0u, mine, 0);  // softmax: the first choice is the largest
+    // the largest chosen logit: the first one, unless a bias decided
+    float m = __shfl_sync(~0u, mine, 0);
+    if constexpr (kBias) {
+      const uint32_t k = warp_max(my_e[u] >= 0 ? order_key(mine) : 0u);
+      m = __uint_as_float(k >> 31 ? k & 0x7fffffffu : ~k);
+    }
     my_w[u] = 0.0f;
-    if (my_e[u] >= 0) my_w[u] = p.sigmoid ? sigmoid_f(mine) : expf(mine - m);
+    if (my_e[u] >= 0) {
+      if (!p.sigmoid) my_w[u] = expf(mine - m);
+      else if (!p.renorm || m >= 0.0f) my_w[u] = sigmoid_f(mine);
+      else if (m >= kLowestScore) my_w[u] = sigmoid_ratio(mine, m);
+    }
     float total = 1.0f;
     if (p.renorm || !p.sigmoid) {
       total = my_w[u];
