@@ -752,7 +752,9 @@ sq_status sq_fp8_gemm_grouped(const uint8_t* Xq8, int64_t X, const uint8_t* Wq8,
  * too; h is not rounded before pre_norm reads it; LayerNorm's variance is
  * taken around the mean).  The order of every sum depends on K and top_k
  * alone, or on M as well through the launch shape; it never depends on timing.
- * A row with a NaN or an infinity gets a non-finite x_scale.  A weight counts
+ * A row of finite values whose squares leave fp32 (above about 1e19, or below
+ * 1e-15 with an eps of nearly 0) is scaled by a power of two and summed again;
+ * a row with a NaN or an infinity gets a non-finite x_scale.  A weight counts
  * as it is: 0 times an infinity is a NaN (an entry outside [0, R) is not).
  */
 typedef struct sq_block_norm_args {

@@ -360,3 +360,64 @@ def test_route_sigmoid_of_far_negative_logits(renorm, use_bias):
     if renorm:
         assert np.allclose(g[[0, 1, 2, 4, 8]].sum(1), 2.5, rtol=1e-5)
         assert (g[[6, 7]] == 0).all()  # scores of 0
+
+
+# ---------------------------------------------------------------------------
+# block norm: rows whose squares leave fp32
+# ---------------------------------------------------------------------------
+
+def _extreme_rows(M, K, dtype, layer):
+    """Rows of finite values at both ends of fp32, the first ones each of another kind, in the
+    stored values of dtype."""
+    rng = _rng(2, K)
+    x = rng.standard_normal((M, K))
+    x[0] *= 1e25
+    x[1] *= 1e35
+    x[2] *= 3e-30
+    x[3] = 0
+    x[3, 5] = 3e38                    # one value near the largest, a row of zeros
+    x[4] = 1e19
+    x[4, ::2] = -1e19                 # squares just in range, their sum not
+    x[5] = rng.uniform(1, 2, K) * 1e36  # the plain sum leaves fp32 too (LayerNorm's mean)
+    x[6] *= 1e-38
+    x[7, :K // 2] *= 1e21             # the sum of the squares would hide the other half
+    return _cuda_of(x).to(dtype)
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["int8", "fp8"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("M,K", [(9, 512), (5, 8192), (9, 9216), (3, 32768), (4000, 512), (2500, 4096)])
+def test_block_norm_of_rows_whose_squares_leave_fp32(M, K, kind, dtype, fp8):
+    """Statistics of finite rows never overflow or vanish: the row's norm, codes and scale are those
+    of the definition, as sq.norm_smooth_quant_per_token's are."""
+    norm = {"rms": sq.NORM_RMS, "layer": sq.NORM_LAYER}[kind]
+    rows = min(M, 8)
+    x = _extreme_rows(max(M, 8), K, dtype, kind == "layer")[:M].contiguous()
+    keep = np.r_[0:rows, max(rows, M - 4):M]
+    for eps in (1e-5, 0.0):
+        for post, pre in ((True, False), (False, True), (True, True)):
+            h, q, s = sq.block_norm_quant_per_token(
+                x, None, post_norm=norm if post else sq.NORM_NONE, post_eps=eps,
+                pre_norm=norm if pre else sq.NORM_NONE, pre_eps=eps, fp8=fp8)
+            name = lambda on: (kind if on else "none", None, None, eps)  # noqa: E731
+            with np.errstate(all="ignore"):
+                hr, dh, y, dy = ref.block_norm(_np64(x[keep]), post=name(post), pre=name(pre))
+            half = 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -23
+            # (below the normal range h is rounded to a multiple of the type's smallest number)
+            tiny = 2.0 ** -133 if dtype == torch.bfloat16 else 2.0 ** -149
+            assert (np.abs(_np64(h[keep]) - hr) <= dh + half * (np.abs(hr) + dh) + tiny).all()
+            vals = ref.E4M3[q[keep].cpu().numpy()] if fp8 else q[keep].cpu().numpy().astype(np.float64)
+            ref.check_codes(vals, _np64(s[keep]), y, dy + 2.0 ** -149, 448.0 if fp8 else 127.0)
+
+
+def test_block_norm_of_extreme_rows_equals_the_norm_call():
+    """Without a norm behind the block the call is sq.norm_smooth_quant_per_token's, whose sums
+    are fp64: the same scales but for fp32 roundings, on both kernels."""
+    for M, K in ((12, 1040), (4000, 512)):
+        x = _extreme_rows(M, K, torch.float32, False)
+        _, q, s = sq.block_norm_quant_per_token(x, pre_norm=sq.NORM_RMS)
+        q1, s1 = sq.norm_smooth_quant_per_token(x, sq.NORM_RMS)
+        assert torch.isfinite(s).all() and (s > 0).all()
+        assert ((s - s1).abs() <= 100 * 2.0 ** -24 * s1).all()
+        assert (q.int() - q1.int()).abs().max() <= 1

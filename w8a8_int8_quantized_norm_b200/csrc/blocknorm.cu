@@ -16,6 +16,7 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <float.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "sq_device.cuh"
@@ -226,27 +227,71 @@ __device__ __forceinline__ uint2 codes_f8(const float2 (&v)[4], float inv) {
   return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
+// The norm's factor 1 / sqrt(mean square + eps) of a row whose sums overflow or
+// vanish in fp32: v (this thread's ch chunks, in local memory) is multiplied by
+// a power of two that brings its largest value near 2^50, eps by its square,
+// LayerNorm's mean taken off, and the squares summed again.  A function of its
+// own on a copy of v: inlined, it took registers from the rows that never need
+// it (16384 x 8192: 156 us without, 176 to 213 inlined, 160 like this).
+__device__ __noinline__ float rescue(float2* v, int ch, int K, bool layer, float eps, float* slot,
+                                     Team tm) {
+  const int own = max(0, min(ch, ((K >> 3) - tm.thread + tm.threads - 1) / tm.threads)) * 4;
+  float am = 0.0f;
+#pragma unroll 1
+  for (int i = 0; i < own; ++i) am = max_nan(am, max_nan(fabsf(v[i].x), fabsf(v[i].y)));
+  tm.sync();  // `slot` has been read
+  am = team_max(am, slot, tm);
+  tm.sync();
+  if (!(am <= FLT_MAX)) return NAN;  // a NaN or an infinity in the row
+  if (am == 0.0f) return rsqrtf(eps);
+  // 2^100 at most, so that an eps this is done for (below 2^-100) stays finite
+  const float c = __uint_as_float(static_cast<uint32_t>(min(50 - ilogbf(am), 100) + 127) << 23);
+  float sum = 0.0f;
+#pragma unroll 1
+  for (int i = 0; i < own; ++i) {
+    v[i] = make_float2(v[i].x * c, v[i].y * c);
+    sum += v[i].x + v[i].y;
+  }
+  float mu = 0.0f;
+  if (layer) {
+    mu = team_sum(sum, slot, tm) / static_cast<float>(K);
+    tm.sync();
+  }
+  sum = 0.0f;
+#pragma unroll 1
+  for (int i = 0; i < own; ++i) {
+    v[i] = make_float2(v[i].x - mu, v[i].y - mu);
+    sum = fmaf(v[i].x, v[i].x, fmaf(v[i].y, v[i].y, sum));
+  }
+  return rsqrtf(team_sum(sum, slot, tm) / static_cast<float>(K) + eps * c * c);
+}
+
 // v (this thread's chunks) -> its norm before gamma and beta, in place.  Two
-// reductions for LayerNorm, one for RMSNorm, none without a norm.
+// reductions for LayerNorm, one for RMSNorm, none without a norm.  Rows with
+// values above about 1e19, a mean that could carry the largest values over, or
+// an eps of nearly 0 and values below 1e-15 go through rescue(); every thread
+// sees the same sums, so all take the same way.
 template <int CH, bool kFull>
 __device__ __forceinline__ void normalise(float2 (&v)[CH][4], int K, int norm, float eps,
                                           float (*slots)[32], const Team& tm) {
   if (norm == SQ_NORM_NONE) return;
   const float inv_k = __frcp_rn(static_cast<float>(K));
   float2 s[2];
+  bool sound = true;
   if (norm == SQ_NORM_LAYER) {
     s[0] = s[1] = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < CH; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) s[j & 1] = __fadd2_rn(s[j & 1], v[i][j]);
-    const float mu =
-        team_sum((s[0].x + s[0].y) + (s[1].x + s[1].y), slots[0], tm) * inv_k;
+    const float mu = team_sum((s[0].x + s[0].y) + (s[1].x + s[1].y), slots[0], tm) * inv_k;
+    sound = fabsf(mu) <= 0x1p96f;  // up to there FLT_MAX - mu rounds to FLT_MAX
+    const float off = sound ? mu : 0.0f;
 #pragma unroll
     for (int i = 0; i < CH; ++i)
       if (kFull || tm.thread + i * tm.threads < (K >> 3)) {  // the rest of v stays zero
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[i][j] = __fadd2_rn(v[i][j], make_float2(-mu, -mu));
+        for (int j = 0; j < 4; ++j) v[i][j] = __fadd2_rn(v[i][j], make_float2(-off, -off));
       }
   }
   s[0] = s[1] = make_float2(0.0f, 0.0f);
@@ -254,9 +299,23 @@ __device__ __forceinline__ void normalise(float2 (&v)[CH][4], int K, int norm, f
   for (int i = 0; i < CH; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) s[j & 1] = __ffma2_rn(v[i][j], v[i][j], s[j & 1]);
-  const float var =
-      team_sum((s[0].x + s[0].y) + (s[1].x + s[1].y), slots[1], tm) * inv_k;
-  const float r = rsqrtf(var + eps);  // within 2 units in the last place
+  const float t =
+      team_sum((s[0].x + s[0].y) + (s[1].x + s[1].y), slots[1], tm) * inv_k + eps;
+  float r;
+  if (sound && t >= 0x1p-100f && t <= FLT_MAX) {
+    r = rsqrtf(t);  // within 2 units in the last place
+  } else {
+    float2 copy[CH][4];
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) copy[i][j] = v[i][j];
+    r = rescue(&copy[0][0], CH, K, norm == SQ_NORM_LAYER, eps, slots[0], tm);
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[i][j] = copy[i][j];
+  }
 #pragma unroll
   for (int i = 0; i < CH; ++i) scale8(v[i], r);
 }
@@ -298,9 +357,10 @@ __device__ __forceinline__ void store_codes(const float2 (&v)[CH][4], const Bloc
 }
 
 // One row per CTA, straight from global memory: few rows, and rows whose
-// parameters and buffers do not fit the pipeline below.
-template <typename T, int CH, int kMaxThreads>
-__global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const BlockNormParams p) {
+// parameters and buffers do not fit the pipeline below.  kFull: every thread has
+// all its chunks (2000 x 16384, LayerNorm: 87 us, 99 with a test per chunk).
+template <typename T, int CH, int kRegs, bool kFull>
+__global__ void __maxnreg__(kRegs) block_norm_kernel(const BlockNormParams p) {
   __shared__ float slots[5][32];
   const sq_block_norm_args& a = p.a;
   const int chunks = p.K >> 3;
@@ -322,7 +382,7 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const BlockNorm
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
         const int c = tm.thread + i * tm.threads;
-        if (c < chunks) {
+        if (kFull || c < chunks) {
           Raw8<T> raw;
           raw.load(a.x, row * a.ldx + c * 8);
           float2 t[4];
@@ -335,7 +395,7 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const BlockNorm
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = tm.thread + i * tm.threads;
-      if (c < chunks) {
+      if (kFull || c < chunks) {
         Raw8<T> raw;
         raw.load(a.x, m * a.ldx + c * 8);
         raw.get(v[i]);
@@ -348,15 +408,15 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const BlockNorm
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = tm.thread + i * tm.threads;
-      if (c < chunks) res[i].load(a.residual, m * a.ld_res + c * 8);
+      if (kFull || c < chunks) res[i].load(a.residual, m * a.ld_res + c * 8);
     }
   }
   const float tg = a.token_gate ? a.token_gate[m] : 1.0f;
-  normalise<CH, false>(v, p.K, a.post_norm, a.post_eps, slots, tm);
+  normalise<CH, kFull>(v, p.K, a.post_norm, a.post_eps, slots, tm);
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = tm.thread + i * tm.threads;
-    if (c < chunks) {
+    if (kFull || c < chunks) {
       if (a.post_gamma) mul8(v[i], GlobalVec{a.post_gamma}, c);
       if (a.post_beta && a.post_norm == SQ_NORM_LAYER) add8(v[i], GlobalVec{a.post_beta}, c);
       if (a.gate) mul8(v[i], GlobalVec{a.gate}, c);
@@ -370,16 +430,16 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const BlockNorm
     }
   }
   if (!a.Xq) return;
-  normalise<CH, false>(v, p.K, a.pre_norm, a.pre_eps, slots + 2, tm);
+  normalise<CH, kFull>(v, p.K, a.pre_norm, a.pre_eps, slots + 2, tm);
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = tm.thread + i * tm.threads;
-    if (c < chunks) {
+    if (kFull || c < chunks) {
       if (a.pre_gamma) mul8(v[i], GlobalVec{a.pre_gamma}, c);
       if (a.pre_beta && a.pre_norm == SQ_NORM_LAYER) add8(v[i], GlobalVec{a.pre_beta}, c);
     }
   }
-  store_codes<CH, false>(v, p, m, slots[4], tm);
+  store_codes<CH, kFull>(v, p, m, slots[4], tm);
 }
 
 // ---------------------------------------------------------------------------
@@ -735,17 +795,14 @@ cudaError_t launch_block_norm_t(const BlockNormParams& p, int sms, int64_t wait_
   // one chunk a thread while 1024 threads cover the row: least latency (1 x 8192
   // 9 us against 17 with four, 37 x 4096 8 against 16); then two (4096 x 9216 in
   // fp32 131 us, with four 140, two CTAs an SM either way), then eight
-  auto threads = [&](int ch) { return static_cast<unsigned>(((chunks + ch - 1) / ch + 31) / 32 * 32); };
-  if (chunks <= 1024) {
-    cfg.blockDim = dim3(threads(1));
-    return cudaLaunchKernelEx(&cfg, block_norm_kernel<T, 1, 1024>, p);
-  }
-  if (chunks <= 2048) {
-    cfg.blockDim = dim3(threads(2));
-    return cudaLaunchKernelEx(&cfg, block_norm_kernel<T, 2, 1024>, p);
-  }
-  cfg.blockDim = dim3(threads(8));
-  return cudaLaunchKernelEx(&cfg, block_norm_kernel<T, 8, 512>, p);
+  const int ch = chunks <= 1024 ? 1 : chunks <= 2048 ? 2 : 8;
+  const int threads = ((chunks + ch - 1) / ch + 31) / 32 * 32;
+  const bool full = chunks == ch * threads;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  auto kern = ch == 1   ? (full ? block_norm_kernel<T, 1, 32, true> : block_norm_kernel<T, 1, 32, false>)
+              : ch == 2 ? (full ? block_norm_kernel<T, 2, 56, true> : block_norm_kernel<T, 2, 56, false>)
+                        : (full ? block_norm_kernel<T, 8, 128, true> : block_norm_kernel<T, 8, 128, false>);
+  return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 }  // namespace
