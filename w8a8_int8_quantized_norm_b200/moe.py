@@ -93,6 +93,9 @@ class MoELayer:
         sq.block_norm_quant_per_token: h = residual_scale * residual + post_norm(sum
         of the experts) * gate ..., and the next norm's codes.  ``block`` are that
         call's norms, gates and outputs.  The stages are ``h.stages``."""
+        if Xq.dim() != 2 or tuple(logits.shape) != (Xq.shape[0], self.E):
+            raise ValueError("logits must be [T, E] = [%d, %d] for Xq [T, H]"
+                             % (Xq.shape[0], self.E))
         gemm = sq.w8a8_gemm_grouped if self.fmt == "int8" else sq.fp8_gemm_grouped
         r = sq.moe_route(logits, self.top_k, self.score, self.bias, self.renormalize, self.scale,
                          stream=stream)
