@@ -656,8 +656,8 @@ sq_status gemm_grouped(const void* Xq, int64_t X, const void* Wq, const float* x
   // (a tile may reach 256 rows past either's end)
   const int64_t top = 0x7fffffff - 512;
   if (X > top || R > top || N > top / E) return SQ_ERR_UNSUPPORTED;
-  // so are tile numbers: at most one tile per 16 rows (and expert) and 128 columns
-  if ((R / 16 + E + 1) * (N / 128 + 1) > 0x3fffffff) return SQ_ERR_UNSUPPORTED;
+  // so are tile numbers
+  if (grouped_tiles(R, E, N, path_hint) > 0x3fffffff) return SQ_ERR_UNSUPPORTED;
   const uintptr_t esz = epi == raw ? 4 : 2;
   if (K % 16 != 0 || !aligned16(Xq) || !aligned16(Wq) ||
       reinterpret_cast<uintptr_t>(out) % esz != 0 || !aligned4(x_scale) || !aligned4(w_scale) ||

@@ -743,7 +743,22 @@ cudaError_t launch(const CUtensorMap& mw, const TokenMaps& mx, const GroupedPara
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// Decode tiles while an expert has few rows: they keep more weight blocks in
+// flight and need no cluster; past 32 rows an expert's weights would be read
+// again for every 32.  Measured, decode / pair: 2 rows of 2 experts 2048 x 1024
+// 10.8 / 13.9 us, 24 rows of each of 64 experts 2048 x 4096 90.9 / 94.6 us, 100
+// rows of each of 16 experts 4000 x 1040 43.9 / 32.7 us, 4096 x 4096 104 / 62 us
+bool pair_tiles(int64_t R, int64_t E, int path_hint) {
+  return path_hint == 1 || (path_hint == 0 && R > 24 * E);
+}
+
 }  // namespace
+
+int64_t grouped_tiles(int64_t R, int64_t E, int64_t N, int path_hint) {
+  const bool pair = pair_tiles(R, E, path_hint);
+  const int64_t pt = pair ? Cfg<true>::PT : Cfg<false>::PT, qt = pair ? Cfg<true>::QT : Cfg<false>::QT;
+  return ((R + qt - 1) / qt + (E < R ? E : R)) * ((N + pt - 1) / pt);
+}
 
 cudaError_t launch_gemm_grouped(const void* Xq, int64_t X, const void* Wq, const float* x_scale,
                                 const float* w_scale, const int32_t* offsets,
@@ -752,12 +767,7 @@ cudaError_t launch_gemm_grouped(const void* Xq, int64_t X, const void* Wq, const
                                 int num_sms, int64_t wait_polls, int* error_word, bool fp8,
                                 cudaStream_t st) {
   const int sms = num_sms > 0 ? num_sms : 148;
-  // decode tiles while an expert has few rows: they keep more weight blocks in
-  // flight and need no cluster; past 32 rows an expert's weights would be read
-  // again for every 32.  Measured, decode / pair: 2 rows of 2 experts 2048 x 1024
-  // 10.8 / 13.9 us, 24 rows of each of 64 experts 2048 x 4096 90.9 / 94.6 us, 100
-  // rows of each of 16 experts 4000 x 1040 43.9 / 32.7 us, 4096 x 4096 104 / 62 us
-  const bool pair = path_hint == 1 || (path_hint == 0 && R > 24 * E);
+  const bool pair = pair_tiles(R, E, path_hint);
   GroupedParams p{};
   p.x_scale = x_scale;
   p.w_scale = w_scale;
@@ -770,14 +780,13 @@ cudaError_t launch_gemm_grouped(const void* Xq, int64_t X, const void* Wq, const
   p.E = static_cast<int>(E);
   p.N = static_cast<int>(N);
   p.k_blocks = static_cast<int>((K + BK - 1) / BK);
-  const int pt = pair ? 256 : 128, qt = pair ? 256 : 32;
+  const int pt = pair ? Cfg<true>::PT : Cfg<false>::PT;
   p.p_blocks = static_cast<int>((N + pt - 1) / pt);
   p.epi = epi;
   p.vec_out = (reinterpret_cast<uintptr_t>(out) & 15u) == 0 && ldo % 8 == 0;
   p.wait_polls = wait_polls;
   p.error_word = error_word;
-  const int64_t max_units = ((R + qt - 1) / qt + (E < R ? E : R)) * p.p_blocks;
-  if (max_units > 0x3fffffff) return cudaErrorInvalidValue;
+  const int64_t max_units = grouped_tiles(R, E, N, path_hint);
   CUtensorMap mw;
   TokenMaps mx;
   bool ok = make_code_map(&mw, Wq, E * N, K, 128);

@@ -142,6 +142,8 @@ cudaError_t launch_moe_route(const void* logits, bool bf16, int64_t T, int E, in
                              cudaStream_t st);
 
 // grouped.cu (the GEMM of rows grouped by expert)
+// Tiles at most, whatever the groups are (R, E, N > 0).
+int64_t grouped_tiles(int64_t R, int64_t E, int64_t N, int path_hint);
 cudaError_t launch_gemm_grouped(const void* Xq, int64_t X, const void* Wq, const float* x_scale,
                                 const float* w_scale, const int32_t* offsets,
                                 const int32_t* row_token, int64_t R, int64_t E, int64_t N,
