@@ -421,3 +421,42 @@ def test_block_norm_of_extreme_rows_equals_the_norm_call():
         assert torch.isfinite(s).all() and (s > 0).all()
         assert ((s - s1).abs() <= 100 * 2.0 ** -24 * s1).all()
         assert (q.int() - q1.int()).abs().max() <= 1
+
+
+# ---------------------------------------------------------------------------
+# errors of earlier calls
+# ---------------------------------------------------------------------------
+
+AFTER_AN_ERROR = """
+import torch
+from w8a8_int8_quantized_norm_b200 import sq
+
+xq = torch.randint(-127, 128, (600, 128), device="cuda", dtype=torch.int8)
+wq = torch.randint(-127, 128, (2, 256, 128), device="cuda", dtype=torch.int8)
+off = torch.tensor([0, 250, 600], device="cuda", dtype=torch.int32)
+torch.cuda.synchronize()
+try:  # a synchronisation inside a capture is an error of the host's call, and ends the capture
+    with torch.cuda.graph(torch.cuda.CUDAGraph()):
+        status = sq.get_device_error()
+except RuntimeError:
+    pass
+assert sq.status_string(status).startswith("SQ_ERR_CUDA"), status
+for path in (1, 2):
+    out = sq.w8a8_gemm_grouped(xq, wq, None, None, off, epi="i32", path_hint=path)
+    for e, rows in ((0, slice(0, 250)), (1, slice(250, 600))):
+        assert torch.equal(out[rows].double(), xq[rows].double() @ wq[e].double().T)
+out = sq.w8a8_gemm_dequant(xq, wq[0], None, None, "i32", path_hint=1)
+assert torch.equal(out.double(), xq.double() @ wq[0].double().T)
+print("right after the error")
+"""
+
+
+def test_grouped_does_not_report_an_earlier_error():
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", AFTER_AN_ERROR], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "right after the error" in r.stdout, r.stdout + r.stderr[-2000:]

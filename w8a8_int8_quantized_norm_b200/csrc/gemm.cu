@@ -1112,16 +1112,14 @@ cudaError_t launch_pair(const Params& prm, const CUtensorMap& mp, const CUtensor
   if (dev >= 0 && dev < 64 && max_clusters[dev] == 0) {
     cfg.gridDim = dim3(2 * max_pairs);
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) n = max_pairs;
+    if ((e = resident_clusters(&n, kern, &cfg)) != cudaSuccess) return e;
     max_clusters[dev] = n;
   }
   int pairs = (dev >= 0 && dev < 64) ? max_clusters[dev] : max_pairs;
   if (pairs > max_pairs) pairs = max_pairs;
   if (pairs > prm.units) pairs = prm.units;
   cfg.gridDim = dim3(2 * pairs);
-  e = cudaLaunchKernelEx(&cfg, kern, mp, mq, prm);
-  if (e != cudaSuccess) return e;
-  return cudaGetLastError();
+  return cudaLaunchKernelEx(&cfg, kern, mp, mq, prm);
 }
 
 int bn_for_tokens(int64_t M) {

@@ -731,16 +731,14 @@ cudaError_t launch(const CUtensorMap& mw, const TokenMaps& mx, const GroupedPara
     int n = dev >= 0 && dev < 64 ? held[dev].load() : 0;
     if (n == 0) {
       cfg.gridDim = dim3(static_cast<unsigned>(clusters * csize));
-      if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0)
-        n = static_cast<int>(clusters);
+      if ((e = resident_clusters(&n, kern, &cfg)) != cudaSuccess) return e;
       if (dev >= 0 && dev < 64) held[dev].store(n);
     }
     if (n < clusters) clusters = n;
   }
   if (max_units < clusters) clusters = max_units;
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * csize));
-  e = cudaLaunchKernelEx(&cfg, kern, mw, mx, prm);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return cudaLaunchKernelEx(&cfg, kern, mw, mx, prm);
 }
 
 // Decode tiles while an expert has few rows: they keep more weight blocks in

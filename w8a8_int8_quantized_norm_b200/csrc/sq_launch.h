@@ -133,6 +133,15 @@ cudaError_t launch_llmint8_combine(const int32_t* acc, int64_t M, int64_t N, int
                                    int64_t ldw, const int32_t* idx, const int32_t* count, int relu,
                                    void* out, int64_t ldo, cudaStream_t st);
 
+// Clusters of `kernel` that the device holds at once.  An error is returned and
+// no longer the runtime's last one, so that no later call reports it as its own.
+template <typename K>
+inline cudaError_t resident_clusters(int* n, K kernel, const cudaLaunchConfig_t* cfg) {
+  const cudaError_t e = cudaOccupancyMaxActiveClusters(n, kernel, cfg);
+  if (e != cudaSuccess) cudaGetLastError();
+  return e == cudaSuccess && *n <= 0 ? cudaErrorInvalidConfiguration : e;
+}
+
 // moe.cu (the router of a layer of experts)
 size_t moe_route_workspace(int64_t T, int64_t E);
 cudaError_t launch_moe_route(const void* logits, bool bf16, int64_t T, int E, int64_t ld, int top_k,
