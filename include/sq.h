@@ -793,7 +793,8 @@ typedef struct sq_block_norm_args {
  * the _fp8 call: step = fl32(max |y| / 448), codes e4m3(fl32(y * fl32(1 / step))),
  * a zero or subnormal step gives step 0 and zero codes).
  * Errors: SQ_ERR_INVALID_ARG (among them an h_out that overlaps x or residual
- *         otherwise than allowed above, or Xq overlapping an input),
+ *         otherwise than allowed above, or Xq overlapping an input; column
+ *         ranges of one buffer, at its stride, do not overlap),
  *         SQ_ERR_ALIGNMENT, SQ_ERR_UNSUPPORTED, SQ_ERR_CUDA.
  */
 sq_status sq_block_norm_quant_per_token(const sq_block_norm_args* args, void* stream);

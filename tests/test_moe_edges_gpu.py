@@ -460,3 +460,38 @@ def test_grouped_does_not_report_an_earlier_error():
     r = subprocess.run([sys.executable, "-c", AFTER_AN_ERROR], cwd=root, capture_output=True, text=True,
                        timeout=300)
     assert r.returncode == 0 and "right after the error" in r.stdout, r.stdout + r.stderr[-2000:]
+
+
+# ---------------------------------------------------------------------------
+# block norm: rows side by side in one buffer
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("M", [7, 5000])
+@pytest.mark.parametrize("order", [(0, 1, 2), (2, 0, 1), (1, 2, 0)])
+def test_block_norm_on_columns_of_one_buffer(order, M):
+    """x, residual and h_out as column ranges of one buffer share no byte, and a gap between them
+    stays as it was."""
+    K, gap = 528, 16
+    buf = torch.randn((M, 3 * (K + gap)), device="cuda").to(torch.bfloat16)
+    x, res, h = (buf[:, i * (K + gap):i * (K + gap) + K] for i in order)
+    kw = dict(post_norm=sq.NORM_RMS, pre_norm=sq.NORM_LAYER)
+    want = sq.block_norm_quant_per_token(x.clone(), res.clone(), **kw)
+    before = buf.clone()
+    got = sq.block_norm_quant_per_token(x, res, h_out=h, **kw)
+    assert got[0] is h
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    h.copy_(before[:, order[2] * (K + gap):order[2] * (K + gap) + K])
+    assert torch.equal(buf, before)
+
+
+def test_block_norm_sums_rows_beside_its_output():
+    R, M, K = 900, 400, 512
+    buf = torch.randn((R, 2 * K), device="cuda")
+    x, h = buf[:, :K], buf[:M, K:]
+    rows = torch.randint(-1, R, (M, 3), device="cuda", dtype=torch.int32)
+    w = torch.rand((M, 3), device="cuda")
+    want = sq.block_norm_quant_per_token(x.clone(), token_row=rows, weights=w, post_norm=sq.NORM_RMS)
+    got = sq.block_norm_quant_per_token(x, token_row=rows, weights=w, post_norm=sq.NORM_RMS, h_out=h)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)

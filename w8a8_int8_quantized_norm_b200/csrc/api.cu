@@ -670,11 +670,26 @@ sq_status gemm_grouped(const void* Xq, int64_t X, const void* Wq, const float* x
                                        fp8, as_stream(stream)));
 }
 
-// Bytes [p, p + n) against [q, q + m).
-bool overlap(const void* p, int64_t n, const void* q, int64_t m) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return p && q && n > 0 && m > 0 && a < b + static_cast<uintptr_t>(m) &&
-         b < a + static_cast<uintptr_t>(n);
+// `rows` rows of `width` bytes, `stride` bytes from one to the next.
+struct Rows {
+  const void* p;
+  int64_t rows, width, stride;
+};
+
+// Whether two matrices share a byte.  With one stride the columns of a common
+// buffer are told apart (the distance modulo the stride clears both widths);
+// with two, the whole ranges count.
+bool overlap(const Rows& x, const Rows& y) {
+  if (!x.p || !y.p || x.rows <= 0 || y.rows <= 0) return false;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+  const auto bytes = [](const Rows& r) {
+    return static_cast<uintptr_t>((r.rows - 1) * r.stride + r.width);
+  };
+  if (a >= b + bytes(y) || b >= a + bytes(x)) return false;
+  if (x.stride != y.stride) return true;
+  const uintptr_t s = static_cast<uintptr_t>(x.stride);
+  const uintptr_t d = b >= a ? (b - a) % s : (s - (a - b) % s) % s;  // y's columns behind x's
+  return d < static_cast<uintptr_t>(x.width) || s - d < static_cast<uintptr_t>(y.width);
 }
 
 sq_status block_norm(const sq_block_norm_args* args, bool fp8, void* stream) {
@@ -706,15 +721,11 @@ sq_status block_norm(const sq_block_norm_args* args, bool fp8, void* stream) {
   if (a.Xq && !a.x_scale) return SQ_ERR_INVALID_ARG;
   // a row may be replaced by its own output, nothing else may share memory
   const int64_t es = dsize(a.dtype);
-  const int64_t nx = rows > 0 ? ((rows - 1) * a.ldx + a.K) * es : 0;
-  const int64_t nr = ((a.M - 1) * a.ld_res + a.K) * es, nh = ((a.M - 1) * a.ld_h + a.K) * es;
-  if (overlap(a.h_out, nh, a.x, nx) && (sum || a.h_out != a.x || a.ld_h != a.ldx))
-    return SQ_ERR_INVALID_ARG;
-  if (overlap(a.h_out, nh, a.residual, nr) && (a.h_out != a.residual || a.ld_h != a.ld_res))
-    return SQ_ERR_INVALID_ARG;
-  if (overlap(a.Xq, a.M * a.K, a.x, nx) || overlap(a.Xq, a.M * a.K, a.residual, nr) ||
-      overlap(a.Xq, a.M * a.K, a.h_out, nh))
-    return SQ_ERR_INVALID_ARG;
+  const Rows x{a.x, rows, a.K * es, a.ldx * es}, res{a.residual, a.M, a.K * es, a.ld_res * es},
+      h{a.h_out, a.M, a.K * es, a.ld_h * es}, codes{a.Xq, a.M, a.K, a.K};
+  if (overlap(h, x) && (sum || a.h_out != a.x || a.ld_h != a.ldx)) return SQ_ERR_INVALID_ARG;
+  if (overlap(h, res) && (a.h_out != a.residual || a.ld_h != a.ld_res)) return SQ_ERR_INVALID_ARG;
+  if (overlap(codes, x) || overlap(codes, res) || overlap(codes, h)) return SQ_ERR_INVALID_ARG;
   int* err = device_error_word();
   if (!err) return SQ_ERR_CUDA;
   return from_cuda(
