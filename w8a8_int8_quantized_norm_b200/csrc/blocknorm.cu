@@ -11,7 +11,8 @@
 // shared-memory exchange each: a barrier per reduction (sum of squares; mean
 // then squares around it for LayerNorm; max |y|).  Everything is fp32: a
 // row's sum runs over at most 64 values per thread and a tree across threads,
-// a relative error of a few 2^-24, below the rounding of its inputs.
+// a relative error of a few 2^-24, below the rounding of its inputs; the few
+// rows whose sums leave fp32's range are scaled and summed again.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -449,13 +450,15 @@ __global__ void __maxnreg__(kRegs) block_norm_kernel(const BlockNormParams p) {
 // residual after this one, so copies are in flight through the reductions and
 // stores; with plain loads the kernel waited for them (long-scoreboard stalls
 // 8.6 of 15 warps, a third of HBM).  Bound by HBM with the rows of two experts
-// (16384 x 8192, RMSNorm twice: 192 us, 6.3 TB/s), close to it without (162 us,
-// 5.8 TB/s).  The parameter vectors (post_gamma * gate,
+// (16384 x 8192, RMSNorm twice: 191 us, 6.3 TB/s), close to it without (160 us,
+// 5.9 TB/s).  The parameter vectors (post_gamma * gate,
 // post_beta * gate, pre_gamma, pre_beta) are put into shared memory once per
 // CTA: read per row through L1 they were more bytes than the row itself.
 // ---------------------------------------------------------------------------
 constexpr int kMaxGroups = 8;
-constexpr int kPipeMaxSum = 4;   // expert rows a token sums, at most
+// Expert rows a token sums, at most.  More were not tried here: they take the
+// one-row kernel (eight rows, 4096 x 4096: 74 us, 54 at HBM's rate).
+constexpr int kPipeMaxSum = 4;
 // Chunks of a thread and threads of a CTA.  Without a sum 64 values a thread
 // measured best (16384 x 8192: 160 us, 178 us with 32 a thread); with one the
 // rows' copies leave room for three groups at 8192 channels, and 32 values a
@@ -739,8 +742,8 @@ __global__ void __launch_bounds__(pipe_max_threads(kSum), 1)
 // Groups of the pipeline for these arguments, or false if it does not pay:
 // fewer than two groups fit (their copies would not overlap a row's
 // reductions), or there are too few rows for every group to have two (the
-// parameters are then copied for one row each).  16384 x 8192: 161 us, one row
-// per CTA 350; 8192 x 4096: 43 against 72.
+// parameters are then copied for one row each).  16384 x 8192: 160 us, one row
+// per CTA 350; 8192 x 4096: 47 against 72.
 bool pipe_shape(const sq_block_norm_args& a, int sms, PipeShape& sh) {
   const int K = static_cast<int>(a.K), es = a.dtype == SQ_BF16 ? 2 : 4;
   const bool sum = a.token_row != nullptr;
@@ -794,7 +797,7 @@ cudaError_t launch_block_norm_t(const BlockNormParams& p, int sms, int64_t wait_
   cfg.gridDim = dim3(static_cast<unsigned>(p.a.M));
   // one chunk a thread while 1024 threads cover the row: least latency (1 x 8192
   // 9 us against 17 with four, 37 x 4096 8 against 16); then two (4096 x 9216 in
-  // fp32 131 us, with four 140, two CTAs an SM either way), then eight
+  // fp32 128 us, with four 140), then eight
   const int ch = chunks <= 1024 ? 1 : chunks <= 2048 ? 2 : 8;
   const int threads = ((chunks + ch - 1) / ch + 31) / 32 * 32;
   const bool full = chunks == ch * threads;

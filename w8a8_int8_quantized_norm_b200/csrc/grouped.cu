@@ -18,10 +18,12 @@
 // token tiles next to each other, so a weight byte comes from HBM once.
 // Tokens are gathered by TMA (tile::gather4: four rows at their own row
 // coordinates per instruction), so sorting the rows by expert never copies them.
-// Measured (int8, 8192 x 4096 weights): 8 groups of 1024 rows 154 us contiguous
-// (3579 TOPS), 175 us gathered, 71 % of the tensor pipe's cycles at 4096 tokens
-// spread unevenly; one token's two experts 15 us (67 MB, 0.65 of HBM).  Bound by
-// the MMA and the delivery of its operands, decode tiles by the weight stream.
+// Measured (int8, 8192 x 4096 weights): 8 groups of 1024 rows 154 to 160 us
+// contiguous (3579 to 3436 TOPS), 175 to 182 us gathered, 71 % of the tensor
+// pipe's cycles at 4096 tokens spread unevenly; one token's two experts 15 us
+// (67 MB, 0.65 of HBM).  Bound by the MMA and the delivery of its operands,
+// decode tiles by the weight stream (fp8, 32 tokens over 59 of 64 experts 2048 x
+// 4096: 83 us, 500 MB).
 // Warp roles as in gemm.cu: 0 producer, 1 MMA issuer, 2-5 epilogue, 6 the
 // issuer's scheduler; 7-10 gather tokens.  Every wait is bounded; one that runs
 // out records SQ_ERR_PIPELINE_TIMEOUT and the CTAs drain and return.
@@ -743,9 +745,16 @@ cudaError_t launch(const CUtensorMap& mw, const TokenMaps& mx, const GroupedPara
 
 // Decode tiles while an expert has few rows: they keep more weight blocks in
 // flight and need no cluster; past 32 rows an expert's weights would be read
-// again for every 32.  Measured, decode / pair: 2 rows of 2 experts 2048 x 1024
-// 10.8 / 13.9 us, 24 rows of each of 64 experts 2048 x 4096 90.9 / 94.6 us, 100
-// rows of each of 16 experts 4000 x 1040 43.9 / 32.7 us, 4096 x 4096 104 / 62 us
+// again for every 32.  The sizes are on the device, so the mean has to decide:
+// even groups turn between 32 and 48 rows, skewed ones earlier.  Decode / pair in
+// us (the timing's own 5 in both), even, and with half of the rows at one expert:
+//   rows an expert          16          24          32          48          96
+//   64 x 2048 x 4096 fp8  90 / 94     90 / 95     90 / 96    111 / 98   153 / 102
+//     skewed              99 / 102   105 / 101   112 / 102   123 / 103  178 / 118
+//   16 x 4000 x 1040      21 / 23     22 / 24     22 / 24     27 / 25    35 / 27
+//     skewed              23 / 25     23 / 25     23 / 26     26 / 25    37 / 27
+//   8 x 8192 x 4096       51 / 55     51 / 55     51 / 55     59 / 57    82 / 58
+//     skewed              51 / 55     55 / 55     56 / 56     61 / 56    91 / 58
 bool pair_tiles(int64_t R, int64_t E, int path_hint) {
   return path_hint == 1 || (path_hint == 0 && R > 24 * E);
 }

@@ -15,8 +15,12 @@
 // arrived in.  The
 // second pass adds, per expert, the counts of all earlier CTAs and experts and
 // scatters.  With one CTA's worth of tokens the first pass scatters itself.
-// Bound by instructions, not by its 6 MB: 16384 tokens, 128 experts, top 8 take
-// 21 us (34 us when every choice searched all of a lane's keys).
+// Bound by latency, neither by its 6 MB (1 us) nor by issue (8.2 M warp
+// instructions, 7 us): each choice is a warp-wide maximum and then a minimum
+// that waits for it, a CTA's two groups of tokens follow one another between
+// barriers, and registers allow one CTA an SM.  16384 tokens, 128 experts, top 8
+// take 21 us, 16.5 of them the first pass; every choice searching all of a
+// lane's keys, 27 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <float.h>
@@ -104,7 +108,8 @@ __device__ __forceinline__ float load_logit(const float* p) { return *p; }
 // expert (-1: none left, or no token) and its weight.  V: experts per lane.
 // Key 0 marks an expert that cannot be chosen (every finite value's key is above
 // it).  Up to 4 keys a lane are sorted first: 6 exchanges, then a choice costs
-// one maximum and a shift (16384 x 128, top 8: 28.6 us against 34.8 searching);
+// one maximum and a shift (16384 x 128, top 8: 28.6 us against 34.8 searching,
+// 7 us of the timing's own in both);
 // 8 and 16 keys would need 28 and 120 exchanges, and are searched.
 template <typename T, int V, int U, bool kBias>
 __device__ __forceinline__ void choose(const RouteParams& p, const int64_t (&t)[U], int64_t t_end,
