@@ -495,3 +495,74 @@ def test_block_norm_sums_rows_beside_its_output():
     got = sq.block_norm_quant_per_token(x, token_row=rows, weights=w, post_norm=sq.NORM_RMS, h_out=h)
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+# ---------------------------------------------------------------------------
+# tokens of many experts
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["int8", "fp8"])
+@pytest.mark.parametrize("M,K,top_k,dtype", [(300, 4096, 8, torch.bfloat16), (40, 8192, 6, torch.bfloat16),
+                                             (2600, 2048, 8, torch.bfloat16), (5, 16384, 16, torch.float32),
+                                             (33, 9216, 5, torch.float32), (1, 32768, 7, torch.bfloat16)])
+def test_block_norm_sums_many_rows(M, K, top_k, dtype, fp8):
+    rng = _rng(3, M, K)
+    R = M * top_k
+    x, res = (_cuda_of(rng.standard_normal((n, K))).to(dtype) for n in (R, M))
+    rows = rng.integers(-1, R + 1, (M, top_k)).astype(np.int32)  # some entries name no row
+    w = rng.uniform(0, 1, (M, top_k)).astype(np.float32)
+    g = rng.uniform(0.5, 1.5, K).astype(np.float32)
+    h, q, s = sq.block_norm_quant_per_token(
+        x, res, token_row=_cuda_of(rows), weights=_cuda_of(w), post_norm=sq.NORM_RMS, post_gamma=_cuda_of(g),
+        residual_scale=0.5, pre_norm=sq.NORM_LAYER, pre_gamma=_cuda_of(g), fp8=fp8)
+    hr, dh, y, dy = ref.block_norm(_np64(x), _np64(res), rows, w.astype(np.float64), ("rms", g, None, 1e-5),
+                                   None, None, 0.5, ("layer", g, None, 1e-5))
+    half = 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -23
+    assert (np.abs(_np64(h) - hr) <= dh + half * (np.abs(hr) + dh)).all()
+    vals = ref.E4M3[q.cpu().numpy()] if fp8 else q.cpu().numpy().astype(np.float64)
+    ref.check_codes(vals, _np64(s), y, dy, 448.0 if fp8 else 127.0)
+
+
+def test_block_norm_without_expert_rows():
+    """A part of the experts that got no row: nothing is read, and h is the residual."""
+    for M in (3, 5000):
+        x = torch.empty((0, 256), device="cuda")
+        res = torch.randn((M, 256), device="cuda")
+        rows = torch.full((M, 2), -1, dtype=torch.int32, device="cuda")
+        w = torch.full((M, 2), float("nan"), device="cuda")
+        h, q, s = sq.block_norm_quant_per_token(x, res, token_row=rows, weights=w, post_norm=sq.NORM_RMS)
+        want = sq.block_norm_quant_per_token(res)
+        for a, b in zip((h, q, s), want):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp8"])
+@pytest.mark.parametrize("top_k,score", [(1, "softmax"), (4, "sigmoid"), (6, "softmax"), (8, "sigmoid")])
+def test_layer_of_tokens_with_several_experts(top_k, score, fmt):
+    """Every stage against its 64-bit form on the stage before, for one expert to all of them."""
+    layer, act, gamma, Xq, xs, logits, res = _layer(fmt, top_k=top_k, score=score)
+    logits[65:] = -float("inf")
+    h, q, s = layer.forward(Xq, xs, logits, res, post_norm=sq.NORM_RMS, post_gamma=gamma)
+    st = h.stages
+    w, e, off, row, tok, bound = ref.route(_np64(logits), top_k, score)
+    assert np.array_equal(st["route"].experts.cpu().numpy(), e)
+    assert np.array_equal(st["route"].token_row.cpu().numpy(), tok)
+    assert (np.abs(_np64(st["route"].weights) - w) <= bound * np.abs(w) + 2.0 ** -126).all()
+    fp8, n = fmt == "fp8", int(off[-1])
+    val = lambda c: ref.E4M3[c.cpu().numpy()] if fp8 else c.cpu().numpy().astype(np.float64)  # noqa: E731
+    a, ha = val(Xq) * _np64(xs)[:, None], val(st["Hq"][:n]) * _np64(st["h_scale"][:n])[:, None]
+    wide = val(layer.gate_up_q) * _np64(layer.gate_up_scale)[:, :, None]
+    narrow = val(layer.down_q) * _np64(layer.down_scale)[:, :, None]
+    gu, y = _np64(st["gate_up"][:n]), _np64(st["down"][:n])
+    for ex in range(8):
+        sl = slice(off[ex], off[ex + 1])
+        for got, left, right in ((gu[sl], a[row[sl]], wide[ex]), (y[sl], ha[sl], narrow[ex])):
+            want = left @ right.T
+            # accumulation (FP8) and the two scales' roundings, then bf16's half step
+            slack = (31 + 8 + 4) * 2.0 ** -23 * (np.abs(left) @ np.abs(right).T)
+            assert (np.abs(got - want) <= slack + 2.0 ** -8 * (np.abs(want) + slack)).all()
+    g = gamma.cpu().numpy()
+    hr, dh, yr, dy = ref.block_norm(y, _np64(res), tok, _np64(st["route"].weights), ("rms", g, None, 1e-5),
+                                    pre=("rms", None, None, 1e-5))
+    assert (np.abs(_np64(h) - hr) <= dh + 2.0 ** -8 * (np.abs(hr) + dh)).all()
+    ref.check_codes(val(q), _np64(s), yr, dy, 448.0 if fp8 else 127.0)
