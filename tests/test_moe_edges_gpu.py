@@ -566,3 +566,27 @@ def test_layer_of_tokens_with_several_experts(top_k, score, fmt):
                                     pre=("rms", None, None, 1e-5))
     assert (np.abs(_np64(h) - hr) <= dh + 2.0 ** -8 * (np.abs(hr) + dh)).all()
     ref.check_codes(val(q), _np64(s), yr, dy, 448.0 if fp8 else 127.0)
+
+
+# ---------------------------------------------------------------------------
+# the scope of a call
+# ---------------------------------------------------------------------------
+
+def test_a_call_leaves_the_current_stream_as_it_was():
+    x = torch.randn((40, 64), device="cuda")
+    outer, side = torch.cuda.Stream(), torch.cuda.Stream()
+    outside = torch.cuda.ExternalStream(side.cuda_stream)
+    default = torch.cuda.current_stream()
+    want = sq.moe_route(x, 2)
+    torch.cuda.synchronize()
+    for stream in (None, default, side, outer, outside):
+        with torch.cuda.stream(outer):
+            got = sq.moe_route(x, 2, stream=stream)
+            assert torch.cuda.current_stream() == outer
+            with pytest.raises(sq.SQError):  # refused inside the scope
+                sq.moe_route(x, 17, stream=stream)
+            assert torch.cuda.current_stream() == outer
+        assert torch.cuda.current_stream() == default
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)

@@ -186,18 +186,41 @@ def _check(status: int, call: str):
         raise SQError(status, call)
 
 
-def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
-
-
 # The current stream's handle and the current device, without building the
 # Python objects around them: a single-token call costs about as much host time
 # as these do (3.2 us of torch.cuda.current_stream() against 0.1 us).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 _raw_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_get_stream = getattr(torch._C, "_cuda_getCurrentStream", None)
+_set_stream = getattr(torch._C, "_cuda_setStream", None)
 _NO_SCOPE = contextlib.nullcontext()
+
+
+def _stream(stream=None):
+    if stream is not None:
+        return ctypes.c_void_p(stream.cuda_stream)
+    if torch.cuda.is_initialized():
+        return ctypes.c_void_p(_raw_stream(_raw_device()))
+    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+
+class _OnStream:
+    """torch.cuda.stream(stream) where the stream's device is current already: a
+    call costs 2 us more in it, 8 us in the general one."""
+    __slots__ = ("stream", "before")
+
+    def __init__(self, stream):
+        self.stream = stream
+
+    def __enter__(self):
+        s = self.stream
+        self.before = _get_stream(s.device_index)
+        _set_stream(stream_id=s.stream_id, device_index=s.device_index, device_type=s.device_type)
+
+    def __exit__(self, *exc):
+        i, index, kind = self.before
+        _set_stream(stream_id=i, device_index=index, device_type=kind)
 
 
 def _scope(device: torch.device, stream):
@@ -208,7 +231,9 @@ def _scope(device: torch.device, stream):
     if stream is not None:
         if stream.device != device:
             raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, device))
-        return torch.cuda.stream(stream)
+        if _raw_device() != device.index or _get_stream is None or _set_stream is None:
+            return torch.cuda.stream(stream)
+        return _OnStream(stream)
     return _NO_SCOPE if _raw_device() == device.index else torch.cuda.device(device)
 
 
